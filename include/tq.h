@@ -128,13 +128,13 @@ typedef struct {
   int n_q_heads;   /* Hq, a multiple of Hkv with Hq / Hkv <= 8 */
   int page_size;   /* must be 16 */
   int window;      /* W >= 0 recent tokens kept float16 */
-  int key_bits;    /* MSE bits of the key code, 1..4 */
+  int key_bits;    /* MSE bits of the key code, 1..4 (8 with int8) */
   int key_qjl;     /* key correction, a tq_key_correction: TQ_KEY_QJL = TurboQuant_prod (QJL sign
                       sketch of the residual, gamma = ||r||); TQ_KEY_MSE = code only; TQ_KEY_EDEN /
                       TQ_KEY_RENORM = code plus one float scale s per key (EDEN's unbiased
                       ||y||^2 / <y, y_hat>; TurboVec's norm / <y, y_hat> divided by the stored
                       norm, the same number), score n s <q', y_hat> */
-  int value_bits;  /* 1..4 */
+  int value_bits;  /* 1..4 (8 with int8) */
   tq_transform_kind kind;
   const float* k_rot;  /* [device] [Hkv][d*d] (dense) or [Hkv][d] signs (FWHT) */
   const float* v_rot;  /* [device] same shape as k_rot                        */
@@ -188,6 +188,18 @@ typedef struct {
    * head_dim == d; window >= 1 (pages are written whole: at a window flush,
    * or by page-aligned direct appends).  Flat tq_quantize_* do not apply. */
   int kivi;
+  /* 8-bit arm.  1: int8 codes with one float scale for a page's keys of a head
+   * and one for its values, in place of the TurboQuant records: s = max |x| /
+   * 127 over the page (float quotient; 0 below the normal range), code =
+   * nearest integer to x / s, ties to even.  NaN takes code 0, an infinity
+   * +-127, and neither sets the scale.  With every page lie the smallest and
+   * largest key code of each channel (tq_select_pages).  No rotation or sketch
+   * (k_rot, v_rot, qjl_s and the codebooks unused; kind ignored); key_bits =
+   * value_bits = 8; key_qjl, key_split, key_norm_u8, qjl_structured, kivi must
+   * be 0; window >= 1 (pages are written whole: at a window flush, or by
+   * page-aligned direct appends).  head_dim < d is zero-padded as above.  Flat
+   * tq_quantize_* do not apply. */
+  int int8;
 } tq_layer_params;
 
 /*
@@ -238,6 +250,13 @@ tq_status tq_quantize_values(const tq_layer_params* p, const void* v, tq_dtype d
  * codes uint32 [16][d key_bits / 32] (code j of a token at bits
  * (j b) mod 32 of word (j b) / 32), value scales float16 [16], value zeros
  * float16 [16], value codes uint32 [16][d value_bits / 32].
+ * 8-bit arm (int8 = 1): int8 [d] smallest and int8 [d] largest key code of each
+ * channel, float key scale, float value scale, 24 zero bytes, then the codes as
+ * code + 128 in a byte, in tensor-core operand order:
+ *   keys   uint8 [2 n][d/64 j][8 g][4 t][16 e]     token 4 (g / 2) + 2 n + g mod 2,
+ *                                                   channel 64 j + 16 t + e
+ *   values uint8 [d/64 j][2 h][8 g][4 t][4 i][4 s]  token 4 t + s,
+ *                                                   channel 64 j + 8 g + 4 h + i
  * Token position p of sequence b, p < n_compressed[b], lives in page
  * block_table[b][p / 16], slot p % 16.  Positions n_compressed[b] ..
  * seq_len[b]-1 are the float16 window; position p lives at ring slot
@@ -293,10 +312,14 @@ size_t tq_subblock_bytes(const tq_layer_params* p);
  *     the oldest 16 are quantized (from their float16 values) into page
  *     block_table[b][n_compressed[b] / 16] and n_compressed[b] += 16.  With
  *     W == 0 it is quantized directly into slot seq_len[b] of its page.
- *     seq_len[b] and n_compressed[b] are updated on the device.
+ *     seq_len[b] and n_compressed[b] are updated on the device.  (8-bit arm: a
+ *     sequence that must flush but has no page to flush into keeps its window
+ *     and counters, and the device error word is set.)
  *   slot_mapping != NULL (direct): [device] int64 [n_tok]; token t is
  *     quantized into pool slot slot_mapping[t] = page * 16 + slot for every
  *     KV head (negative entries are skipped).  Counters are not touched.
+ *     KIVI and 8-bit arms: every 16 consecutive tokens are one page's slots in
+ *     order, or all negative; a page is written at most once in a call.
  */
 tq_status tq_append_page(const tq_layer_params* p, tq_cache* cache, const void* k, const void* v,
                          tq_dtype dtype, int64_t n_tok, const int64_t* slot_mapping,
@@ -393,6 +416,104 @@ size_t tq_prefill_workspace_size(const tq_layer_params* p, int batch, int n_quer
 tq_status tq_prefill_attention(const tq_layer_params* p, const tq_cache* cache, int n_query, const void* q,
                                tq_dtype dtype, float scale, float* out, float* lse, void* workspace,
                                size_t workspace_bytes, int max_ctx, tq_stream_t stream);
+
+/*
+ * tq_read_cache -- the values that a cache of the 8-bit arm stands for: code times
+ * scale for tokens in pages, the float16 row for tokens in the window, rounded
+ * once to dtype.  The counterpart of tq_prefill_cache, for handing a sequence to a
+ * dense attention, another layer format or another cache.
+ *   k, v    [device] out, [batch][n_tok][Hkv][head_dim] in dtype, 16-byte aligned:
+ *           row i of sequence b is position first + i; rows of positions >=
+ *           seq_len[b] are left as they were
+ * first, n_tok >= 0, first + n_tok <= 2^31 - 64.  TQ_ERR_UNSUPPORTED for other arms.
+ */
+tq_status tq_read_cache(const tq_layer_params* p, const tq_cache* cache, void* k, void* v, tq_dtype dtype, int first,
+                        int n_tok, tq_stream_t stream);
+
+/*
+ * tq_select_pages -- the pages of every (sequence, KV head) that its queries may
+ * weigh most, from the channel bounds of the 8-bit arm's pages.
+ *   qi  = the G queries of the group on one int8 grid (scale max |q| / 127 over
+ *         the group, codes as in the pages)
+ *   I_g = sum_j max(qi_gj kmin_j, qi_gj kmax_j), an integer: no token of the page
+ *         has a larger product of codes with qi_g
+ *   score(page) = float(max_g I_g) * key scale (one float rounding)
+ * The first n_sink and the last n_recent full pages are always taken, the rest of
+ * the n_sel by descending score, the lower page among equals.  The window is not
+ * listed (decode always reads it).  A sequence with at most n_sel full pages
+ * takes them all.
+ *   q          [device] [batch][Hq][head_dim] in dtype
+ *   n_sel      >= 1; n_sink, n_recent >= 0, n_sink + n_recent <= n_sel
+ *   pages      [device] out, int32 [batch][Hkv][n_sel]: page ordinals (token
+ *              position / 16), ascending, -1 behind the last
+ *   counts     [device] out, int32 [batch][Hkv]: pages taken
+ *   workspace  [device] 256-byte aligned, >= tq_select_workspace_size bytes
+ *   max_ctx    upper bound on every seq_len[b]
+ * A sequence whose counters are no valid state gets count 0 and sets
+ * TQ_DEVERR_SEQ_LEN.  TQ_ERR_UNSUPPORTED for other arms.
+ */
+size_t tq_select_workspace_size(const tq_layer_params* p, int batch, int max_ctx);
+tq_status tq_select_pages(const tq_layer_params* p, const tq_cache* cache, const void* q, tq_dtype dtype, int n_sel,
+                          int n_sink, int n_recent, int32_t* pages, int32_t* counts, void* workspace,
+                          size_t workspace_bytes, int max_ctx, tq_stream_t stream);
+
+/*
+ * tq_decode_attention_pages -- tq_decode_attention over the listed pages and the
+ * window only (8-bit arm): softmax, output and lse are of those tokens.
+ *   pages      [device] int32 [batch][Hkv][n_sel] page ordinals in any order; a
+ *              page listed twice counts twice; an ordinal outside the sequence's
+ *              pages is skipped and sets TQ_DEVERR_PAGE_INDEX
+ *   counts     [device] int32 [batch][Hkv]: entries to read, 0..n_sel
+ * Other arguments as in tq_decode_attention; the workspace has
+ * tq_decode_pages_workspace_size bytes.
+ */
+size_t tq_decode_pages_workspace_size(const tq_layer_params* p, int batch, int n_sel, int n_splits);
+tq_status tq_decode_attention_pages(const tq_layer_params* p, const tq_cache* cache, const void* q, tq_dtype dtype,
+                                    float scale, const int32_t* pages, const int32_t* counts, int n_sel, float* out,
+                                    float* lse, void* workspace, size_t workspace_bytes, int max_ctx, int n_splits,
+                                    tq_stream_t stream);
+
+/*
+ * tq_track_pages -- adds a decode step's attention weights to the totals of the
+ * pages (every arm):
+ *   mass[b][page] += sum over the Hq heads and the page's tokens of
+ *                    exp(scores[b][h][t] - lse[b][h])
+ *   scores  [device] float [batch][Hq][max_ctx], lse float [batch][Hq]: as
+ *           tq_decode_attention wrote them for this cache state
+ *   mass    [device] in/out, float [batch][max_pages_per_seq], zeroed by the
+ *           caller for a new sequence; pages without tokens are left as they were
+ * The sums' order is fixed: equal inputs give equal bits.
+ */
+tq_status tq_track_pages(const tq_layer_params* p, const tq_cache* cache, const float* scores, const float* lse,
+                         float* mass, int max_ctx, tq_stream_t stream);
+
+/*
+ * tq_evict_pages -- thins every sequence to its `budget` heaviest full pages (every
+ * arm; keys carry their positions from before the cache, so pages move freely).
+ * The first n_sink and the last n_recent full pages always stay, the rest by
+ * descending mass, the lower page among equals (a NaN counts least).  A sequence
+ * with at most `budget` full pages keeps its state.  With e pages dropped:
+ *   block table   kept pages in their order, then a partly filled page (window ==
+ *                 0), then the dropped pages in theirs (the sequence fills them
+ *                 again first), then the other entries unchanged
+ *   counters      seq_len and n_compressed fall by 16 e
+ *   window        row of position p moves to the slot of p - 16 e
+ *   mass_after    the kept pages' masses in their order (and the partly filled
+ *                 page's), zeros behind
+ *   kept          [device] out, nullable, int32 [batch][budget]: ordinals of the
+ *                 kept pages before the call, -1 behind the last
+ * `after` receives the table, counters and window: it is the cache itself (in
+ * place), or another descriptor over the same page pool with the same batch and
+ * max_pages_per_seq and its own buffers for all of them, which the call overwrites
+ * (its block_table is written although the type is const).  mass_after may be
+ * mass.  In place the window may hold up to 12784 tokens (TQ_ERR_UNSUPPORTED above).
+ *   workspace  [device] 256-byte aligned, >= tq_evict_workspace_size bytes
+ * A sequence whose counters are no valid state keeps it and sets TQ_DEVERR_SEQ_LEN.
+ */
+size_t tq_evict_workspace_size(const tq_layer_params* p, int batch, int max_pages_per_seq);
+tq_status tq_evict_pages(const tq_layer_params* p, const tq_cache* cache, tq_cache* after, const float* mass,
+                         float* mass_after, int budget, int n_sink, int n_recent, int32_t* kept, void* workspace,
+                         size_t workspace_bytes, tq_stream_t stream);
 
 /* Synchronises the stream, reads and clears the device error word.
  * Returns TQ_ERR_DEVICE_CHECK if any bit was set (bits in *bits_out, nullable). */

@@ -16,14 +16,17 @@ import numpy as np
 from . import _lib
 from ._lib import (KEY_EDEN, KEY_MSE, KEY_QJL, KEY_RENORM, PAGE_SIZE, ROLE_KEY_ROT, ROLE_QJL, ROLE_QJL_SIGNS, ROLE_VALUE_ROT, TQ_BF16, TQ_DENSE, TQ_F16, TQ_F32, TQ_FWHT,
                    Cache, LayerParams, TQError, append_page, build_codebook, build_transform, check_device_error,
-                   decode_attention, decode_workspace_size, prefill_attention, prefill_cache, prefill_workspace_size,
-                   quantize_keys, quantize_values, subblock_bytes)
+                   decode_attention, decode_attention_pages, decode_pages_workspace_size, decode_workspace_size, evict_pages,
+                   evict_workspace_size, prefill_attention, prefill_cache, prefill_workspace_size, quantize_keys,
+                   quantize_values, read_cache, select_pages, select_workspace_size, subblock_bytes, track_pages)
 
 __all__ = [
     "TQLayer", "PagedCache", "LayerParams", "Cache", "TQError", "build_codebook", "build_transform",
     "quantize_keys", "quantize_values", "append_page", "decode_workspace_size", "decode_attention",
     "prefill_workspace_size", "prefill_attention", "prefill_cache", "norm_range_for", "bits_per_channel",
     "check_device_error", "subblock_bytes", "TQ_DENSE", "TQ_FWHT", "TQ_F32", "TQ_BF16", "TQ_F16", "PAGE_SIZE",
+    "read_cache", "select_workspace_size", "select_pages", "decode_pages_workspace_size", "decode_attention_pages",
+    "track_pages", "evict_workspace_size", "evict_pages",
     "ROLE_KEY_ROT", "ROLE_VALUE_ROT", "ROLE_QJL", "ROLE_QJL_SIGNS", "KEY_MSE", "KEY_QJL", "KEY_EDEN", "KEY_RENORM",
 ]
 
@@ -57,7 +60,7 @@ class TQLayer:
                  window: int = 0, key_qjl: int = KEY_QJL, seed: int = 0, layer: int = 0, device="cuda",
                  head_dim: int | None = None, key_split: bool = False,
                  key_norm_range: tuple[float, float] | None = None, qjl_structured: bool = False,
-                 kivi: bool = False):
+                 kivi: bool = False, int8: bool = False):
         """d: the transform and code dimension (128 or 256); head_dim (default d):
         the length of the vectors the caller passes, zero-padded to d inside
         the kernels (a multiple of 8 in (d/2, d]).  key_qjl: the key
@@ -72,7 +75,10 @@ class TQLayer:
         applied as a fast Walsh-Hadamard transform, instead of a dense Gaussian.
         kivi: the KIVI-like control arm (asymmetric min-max codes of key_bits /
         value_bits = 2 or 4 bits, keys per channel over a page, values per
-        token; no rotation; key_qjl must be KEY_MSE and window >= 1)."""
+        token; no rotation; key_qjl must be KEY_MSE and window >= 1).
+        int8: the 8-bit arm (key_bits = value_bits = 8, one scale for a page of
+        a head's keys and one for its values; no rotation; key_qjl must be
+        KEY_MSE and window >= 1)."""
         import torch
 
         self.d, self.n_kv_heads, self.n_q_heads = d, n_kv_heads, n_q_heads
@@ -82,11 +88,12 @@ class TQLayer:
         if self.key_qjl not in (KEY_MSE, KEY_QJL, KEY_EDEN, KEY_RENORM):
             raise ValueError(f"key_qjl must be one of KEY_MSE, KEY_QJL, KEY_EDEN, KEY_RENORM, got {key_qjl}")
         self.key_split, self.key_norm_range = bool(key_split), key_norm_range
-        self.kivi = bool(kivi)
-        self.k_cb = build_codebook(d, key_bits)
+        self.kivi, self.int8 = bool(kivi), bool(int8)
+        self.k_cb = self.v_cb = None
+        if not self.int8:
+            self.k_cb, self.v_cb = build_codebook(d, key_bits), build_codebook(d, value_bits)
         self.k_cb_hi = build_codebook(d, key_bits + 1) if key_split else None
-        self.v_cb = build_codebook(d, value_bits)
-        if self.kivi:  # no transforms
+        if self.kivi or self.int8:  # no transforms
             self.k_rot_host = self.v_rot_host = self.k_rot = self.v_rot = None
         else:
             kr = np.stack([build_transform(kind, d, seed, layer, h, ROLE_KEY_ROT) for h in range(n_kv_heads)])
@@ -108,9 +115,9 @@ class TQLayer:
         p.head_dim = self.head_dim
         p.k_rot = self.k_rot.data_ptr() if self.k_rot is not None else None
         p.v_rot = self.v_rot.data_ptr() if self.v_rot is not None else None
-        p.kivi = int(self.kivi)
+        p.kivi, p.int8 = int(self.kivi), int(self.int8)
         p.qjl_s = self.qjl_s.data_ptr() if self.qjl_s is not None else None
-        for name, (c, t, _) in (("k", self.k_cb), ("v", self.v_cb)):
+        for name, (c, t, _) in () if self.int8 else (("k", self.k_cb), ("v", self.v_cb)):
             getattr(p, f"{name}_centroids")[: len(c)] = [float(x) for x in c]
             getattr(p, f"{name}_bounds")[: len(t)] = [float(x) for x in t]
         if key_split:
@@ -175,6 +182,12 @@ class PagedCache:
         straight into their pages, the last W .. W + 15 tokens go to the float16 window, and
         the counters are set, as live decoding would leave them."""
         prefill_cache(self.layer.params, self.cache, k.contiguous(), v.contiguous(), k.shape[1], stream)
+
+    def share_pages(self, other: "PagedCache") -> None:
+        """Refer to another cache's page pool (same layer layout) instead of an own one: this cache keeps its own
+        block table, counters and window, as the outcome of `evict_pages` or a second reader of the pages."""
+        self.pool, self.n_pages = other.pool, other.n_pages
+        self.cache.page_pool, self.cache.n_pages = other.cache.page_pool, other.cache.n_pages
 
     def append(self, k, v, stream=None) -> None:
         """One decode step: k, v [batch, Hkv, d]."""

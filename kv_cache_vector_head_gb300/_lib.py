@@ -27,7 +27,11 @@ EXPORTED = [
     "tq_build_codebook", "tq_build_transform", "tq_quantize_keys", "tq_quantize_values", "tq_subblock_bytes",
     "tq_append_page", "tq_decode_workspace_size", "tq_decode_attention", "tq_check_device_error", "tq_last_error",
     "tq_decode_attention_static", "tq_prefill_workspace_size", "tq_prefill_attention", "tq_prefill_cache",
+    "tq_read_cache", "tq_select_workspace_size", "tq_select_pages", "tq_decode_pages_workspace_size",
+    "tq_decode_attention_pages", "tq_track_pages", "tq_evict_workspace_size", "tq_evict_pages",
 ]
+SIZES = ["tq_subblock_bytes", "tq_decode_workspace_size", "tq_prefill_workspace_size", "tq_select_workspace_size",
+         "tq_decode_pages_workspace_size", "tq_evict_workspace_size"]  # exports that return a size_t
 STATIC_SCRATCH_BYTES = 16 << 20
 
 
@@ -47,7 +51,7 @@ class LayerParams(ctypes.Structure):
         ("head_dim", c_int),
         ("key_split", c_int), ("k_hi_centroids", c_float * 16), ("k_hi_bounds", c_float * 16),
         ("key_norm_u8", c_int), ("key_norm_log2_lo", c_float), ("key_norm_log2_hi", c_float),
-        ("qjl_structured", c_int), ("kivi", c_int),
+        ("qjl_structured", c_int), ("kivi", c_int), ("int8", c_int),
     ]
 
 
@@ -75,25 +79,35 @@ def lib():
                                        c_void_p, c_void_p]
         L.tq_quantize_values.argtypes = [POINTER(LayerParams), c_void_p, c_int, c_int64, c_void_p, c_void_p, c_void_p]
         L.tq_subblock_bytes.argtypes = [POINTER(LayerParams)]
-        L.tq_subblock_bytes.restype = c_size_t
         L.tq_append_page.argtypes = [POINTER(LayerParams), POINTER(Cache), c_void_p, c_void_p, c_int, c_int64,
                                      c_void_p, c_void_p]
         L.tq_prefill_cache.argtypes = [POINTER(LayerParams), POINTER(Cache), c_void_p, c_void_p, c_int, c_int, c_void_p]
         L.tq_decode_workspace_size.argtypes = [POINTER(LayerParams), c_int, c_int, c_int]
-        L.tq_decode_workspace_size.restype = c_size_t
         L.tq_decode_attention.argtypes = [POINTER(LayerParams), POINTER(Cache), c_void_p, c_int, c_float, c_void_p,
                                           c_void_p, c_void_p, c_void_p, c_size_t, c_int, c_int, c_void_p]
         L.tq_decode_attention_static.argtypes = [POINTER(LayerParams), POINTER(Cache), c_void_p, c_int, c_float,
                                                  c_void_p, c_void_p, c_void_p, c_int, c_int, c_void_p]
         L.tq_prefill_workspace_size.argtypes = [POINTER(LayerParams), c_int, c_int, c_int]
-        L.tq_prefill_workspace_size.restype = c_size_t
         L.tq_prefill_attention.argtypes = [POINTER(LayerParams), POINTER(Cache), c_int, c_void_p, c_int, c_float,
                                            c_void_p, c_void_p, c_void_p, c_size_t, c_int, c_void_p]
+        L.tq_read_cache.argtypes = [POINTER(LayerParams), POINTER(Cache), c_void_p, c_void_p, c_int, c_int, c_int, c_void_p]
+        L.tq_select_workspace_size.argtypes = [POINTER(LayerParams), c_int, c_int]
+        L.tq_select_pages.argtypes = [POINTER(LayerParams), POINTER(Cache), c_void_p, c_int, c_int, c_int, c_int, c_void_p,
+                                      c_void_p, c_void_p, c_size_t, c_int, c_void_p]
+        L.tq_decode_pages_workspace_size.argtypes = [POINTER(LayerParams), c_int, c_int, c_int]
+        L.tq_decode_attention_pages.argtypes = [POINTER(LayerParams), POINTER(Cache), c_void_p, c_int, c_float, c_void_p,
+                                                c_void_p, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_int, c_int,
+                                                c_void_p]
+        L.tq_track_pages.argtypes = [POINTER(LayerParams), POINTER(Cache), c_void_p, c_void_p, c_void_p, c_int, c_void_p]
+        L.tq_evict_workspace_size.argtypes = [POINTER(LayerParams), c_int, c_int]
+        L.tq_evict_pages.argtypes = [POINTER(LayerParams), POINTER(Cache), POINTER(Cache), c_void_p, c_void_p, c_int, c_int,
+                                     c_int, c_void_p, c_void_p, c_size_t, c_void_p]
+        for name in SIZES:
+            getattr(L, name).restype = c_size_t
         L.tq_check_device_error.argtypes = [c_void_p, POINTER(c_uint32)]
         L.tq_last_error.restype = ctypes.c_char_p
         for name in EXPORTED:
-            if name not in ("tq_subblock_bytes", "tq_decode_workspace_size", "tq_prefill_workspace_size",
-                            "tq_last_error"):
+            if name not in SIZES and name != "tq_last_error":
                 getattr(L, name).restype = c_int
         _lib = L
     return _lib
@@ -206,6 +220,68 @@ def prefill_attention(p: LayerParams, cache: Cache, n_query: int, q, scale: floa
     _check(lib().tq_prefill_attention(ctypes.byref(p), ctypes.byref(cache), n_query, _ptr(q), dtype_code(q), scale,
                                       _ptr(out), _ptr(lse), _ptr(workspace),
                                       workspace.numel() * workspace.element_size(), max_ctx, _stream(stream)))
+
+
+def _size(n: int) -> int:
+    if n == 0:
+        _check(TQ_ERR_INVALID_ARG)
+    return n
+
+
+def _nbytes(t) -> int:
+    return t.numel() * t.element_size()
+
+
+def read_cache(p: LayerParams, cache: Cache, k, v, first: int, n_tok: int, stream=None) -> None:
+    """The values that positions first .. first + n_tok - 1 of every sequence stand for (int8 layers):
+    k, v [batch, n_tok, Hkv, head_dim]; rows of positions that a sequence does not have stay as they are."""
+    if k.dtype != v.dtype:
+        raise TypeError(f"k and v must have one dtype, got {k.dtype} and {v.dtype}")
+    _check(lib().tq_read_cache(ctypes.byref(p), ctypes.byref(cache), _ptr(k), _ptr(v), dtype_code(k), first, n_tok,
+                               _stream(stream)))
+
+
+def select_workspace_size(p: LayerParams, batch: int, max_ctx: int) -> int:
+    return _size(lib().tq_select_workspace_size(ctypes.byref(p), batch, max_ctx))
+
+
+def select_pages(p: LayerParams, cache: Cache, q, n_sel: int, n_sink: int, n_recent: int, pages, counts, workspace,
+                 max_ctx: int, stream=None) -> None:
+    """The n_sel pages of every (sequence, KV head) that its queries may weigh most (int8 layers): pages int32
+    [batch, Hkv, n_sel] ascending, -1 behind, counts int32 [batch, Hkv]; q [batch, Hq, head_dim]."""
+    _check(lib().tq_select_pages(ctypes.byref(p), ctypes.byref(cache), _ptr(q), dtype_code(q), n_sel, n_sink, n_recent,
+                                 _ptr(pages), _ptr(counts), _ptr(workspace), _nbytes(workspace), max_ctx, _stream(stream)))
+
+
+def decode_pages_workspace_size(p: LayerParams, batch: int, n_sel: int, n_splits: int = 0) -> int:
+    return _size(lib().tq_decode_pages_workspace_size(ctypes.byref(p), batch, n_sel, n_splits))
+
+
+def decode_attention_pages(p: LayerParams, cache: Cache, q, scale: float, pages, counts, n_sel: int, out, lse, workspace,
+                           max_ctx: int, n_splits: int = 0, stream=None) -> None:
+    """decode_attention over the listed pages and the window only (int8 layers); pages, counts as select_pages gives them."""
+    _check(lib().tq_decode_attention_pages(ctypes.byref(p), ctypes.byref(cache), _ptr(q), dtype_code(q), scale, _ptr(pages),
+                                           _ptr(counts), n_sel, _ptr(out), _ptr(lse), _ptr(workspace), _nbytes(workspace),
+                                           max_ctx, n_splits, _stream(stream)))
+
+
+def track_pages(p: LayerParams, cache: Cache, scores, lse, mass, max_ctx: int, stream=None) -> None:
+    """Adds a decode step's attention weights to the pages' totals: scores [batch, Hq, max_ctx] and lse [batch, Hq] from
+    decode_attention, mass float32 [batch, max_pages_per_seq]."""
+    _check(lib().tq_track_pages(ctypes.byref(p), ctypes.byref(cache), _ptr(scores), _ptr(lse), _ptr(mass), max_ctx,
+                                _stream(stream)))
+
+
+def evict_workspace_size(p: LayerParams, batch: int, max_pages_per_seq: int) -> int:
+    return _size(lib().tq_evict_workspace_size(ctypes.byref(p), batch, max_pages_per_seq))
+
+
+def evict_pages(p: LayerParams, cache: Cache, after: Cache, mass, mass_after, budget: int, n_sink: int, n_recent: int, kept,
+                workspace, stream=None) -> None:
+    """Keeps the `budget` heaviest full pages of every sequence; `after` is `cache` itself or another cache over the same
+    pool; kept int32 [batch, budget] (or None): the kept pages' ordinals before, -1 behind."""
+    _check(lib().tq_evict_pages(ctypes.byref(p), ctypes.byref(cache), ctypes.byref(after), _ptr(mass), _ptr(mass_after),
+                                budget, n_sink, n_recent, _ptr(kept), _ptr(workspace), _nbytes(workspace), _stream(stream)))
 
 
 def check_device_error(stream=None) -> int:

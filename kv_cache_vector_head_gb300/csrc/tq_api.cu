@@ -8,6 +8,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "tq_int8.cuh"
 #include "tq_internal.h"
 #include "tq_launch.h"
 
@@ -48,7 +49,13 @@ static tq_status make_params(const tq_layer_params* p, KParams* K, bool need_dev
   if (p->n_q_heads / p->n_kv_heads > TQ_MAX_GQA) return fail(TQ_ERR_UNSUPPORTED, "n_q_heads / n_kv_heads must be <= 8");
   if (p->page_size != TQ_PAGE_SIZE) return fail(TQ_ERR_UNSUPPORTED, "page_size must be 16");
   if (p->window < 0) return fail(TQ_ERR_INVALID_ARG, "window must be >= 0");
-  if (p->key_bits < 1 || p->key_bits > TQ_MAX_BITS || p->value_bits < 1 || p->value_bits > TQ_MAX_BITS)
+  if (p->int8 != 0 && p->int8 != 1) return fail(TQ_ERR_INVALID_ARG, "int8 must be 0 or 1");
+  if (p->int8) {
+    if (p->key_bits != 8 || p->value_bits != 8) return fail(TQ_ERR_INVALID_ARG, "int8: key_bits and value_bits must be 8");
+    if (p->key_qjl || p->key_split || p->key_norm_u8 || p->qjl_structured || p->kivi)
+      return fail(TQ_ERR_INVALID_ARG, "int8: key_qjl, key_split, key_norm_u8, qjl_structured, kivi must be 0");
+    if (p->window < 1) return fail(TQ_ERR_INVALID_ARG, "int8: window must be >= 1 (pages are written whole)");
+  } else if (p->key_bits < 1 || p->key_bits > TQ_MAX_BITS || p->value_bits < 1 || p->value_bits > TQ_MAX_BITS)
     return fail(TQ_ERR_UNSUPPORTED, "key_bits and value_bits must be 1..4");
   if (p->key_qjl < 0 || p->key_qjl > 3) return fail(TQ_ERR_INVALID_ARG, "key_qjl must be 0..3 (see tq_key_correction)");
   if (p->kind != TQ_DENSE && p->kind != TQ_FWHT) return fail(TQ_ERR_INVALID_ARG, "bad transform kind");
@@ -77,12 +84,13 @@ static tq_status make_params(const tq_layer_params* p, KParams* K, bool need_dev
   if (p->key_norm_u8 && !(std::isfinite(p->key_norm_log2_lo) && std::isfinite(p->key_norm_log2_hi) &&
                           p->key_norm_log2_lo < p->key_norm_log2_hi))
     return fail(TQ_ERR_INVALID_ARG, "key_norm_u8 needs finite key_norm_log2_lo < key_norm_log2_hi");
-  if (need_device_ptrs && !p->kivi) {
+  if (need_device_ptrs && !p->kivi && !p->int8) {
     if (!p->k_rot || !p->v_rot) return fail(TQ_ERR_INVALID_ARG, "null k_rot / v_rot");
     if (p->key_qjl == TQ_KEY_QJL && !p->qjl_s) return fail(TQ_ERR_INVALID_ARG, "null qjl_s with key_qjl");
     if (!aligned(p->k_rot, 16) || !aligned(p->v_rot, 16) || (p->qjl_s && !aligned(p->qjl_s, 16)))
       return fail(TQ_ERR_INVALID_ARG, "transforms must be 16-byte aligned");
   }
+  *K = KParams{};
   K->d = p->d;
   K->dh = p->head_dim ? p->head_dim : p->d;
   K->hkv = p->n_kv_heads;
@@ -102,6 +110,12 @@ static tq_status make_params(const tq_layer_params* p, KParams* K, bool need_dev
     K->kt[i] = p->k_bounds[i];
     K->vc[i] = p->v_centroids[i];
     K->vt[i] = p->v_bounds[i];
+  }
+  K->int8 = p->int8;
+  K->kivi = p->kivi;
+  if (p->int8) {  // no transform and no codebook: the page layout is all that the kernels take
+    K->sub_bytes = i8_sub_bytes(p->d);
+    return TQ_OK;
   }
   // Walsh coefficients a_S = 2^-(b-1) sum_m c(m) (-1)^popcount(m & S), c(m) = C[half + m]
   auto walsh = [](const float* c, int bits, float* a) {
@@ -198,12 +212,18 @@ static tq_status make_cache(const tq_cache* c, const KParams& K, KCache* C, bool
   return TQ_OK;
 }
 
+// Decode workspace of either kind of layer (8-bit arm: pages and window in groups of 16 tokens).
+static WsLayout decode_layout(const KParams& K, int batch, int max_ctx, int n_splits) {
+  if (K.int8) return int8_ws_layout(K, batch, (long long)(max_ctx + TQ_PAGE_SIZE - 1) / TQ_PAGE_SIZE + 1, n_splits, num_sms());
+  return decode_ws_layout(K, batch, max_ctx, n_splits, num_sms());
+}
+
 // Prefill workspace: the virtual sequences' counters and parent rows, then a decode workspace
 // for batch * n_query sequences.
 static size_t prefill_layout(const KParams& K, int batch, int n_query, int max_ctx, WsLayout* L) {
   const size_t head = ((size_t)3 * batch * n_query * sizeof(int32_t) + 255) & ~(size_t)255;
-  const int S = prefill_tiles_ok(K) ? prefill_tile_splits(K, batch, n_query, max_ctx, num_sms()) : 0;
-  *L = decode_ws_layout(K, batch * n_query, max_ctx, S, num_sms());
+  const int S = !K.int8 && prefill_tiles_ok(K) ? prefill_tile_splits(K, batch, n_query, max_ctx, num_sms()) : 0;
+  *L = decode_layout(K, batch * n_query, max_ctx, S);
   return head + L->total;
 }
 
@@ -227,6 +247,7 @@ extern "C" tq_status tq_quantize_keys(const tq_layer_params* p, const void* k, t
   tq_status s = make_params(p, &K, true);
   if (s != TQ_OK) return s;
   if ((s = check_dtype(dtype)) != TQ_OK) return s;
+  if (K.int8) return fail(TQ_ERR_UNSUPPORTED, "int8: keys are quantized into pages only");
   if (K.kivi) return fail(TQ_ERR_UNSUPPORTED, "kivi: keys are quantized into pages only");
   if (n_vec < 0) return fail(TQ_ERR_INVALID_ARG, "n_vec < 0");
   if (n_vec == 0) return ok();
@@ -246,6 +267,7 @@ extern "C" tq_status tq_quantize_values(const tq_layer_params* p, const void* v,
   tq_status s = make_params(p, &K, true);
   if (s != TQ_OK) return s;
   if ((s = check_dtype(dtype)) != TQ_OK) return s;
+  if (K.int8) return fail(TQ_ERR_UNSUPPORTED, "int8: values are quantized into pages only");
   if (K.kivi) return fail(TQ_ERR_UNSUPPORTED, "kivi: values are quantized into pages only");
   if (n_vec < 0) return fail(TQ_ERR_INVALID_ARG, "n_vec < 0");
   if (n_vec == 0) return ok();
@@ -270,10 +292,15 @@ extern "C" tq_status tq_append_page(const tq_layer_params* p, tq_cache* cache, c
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   if (slot_mapping == nullptr) {
     if (n_tok != cache->batch) return fail(TQ_ERR_INVALID_ARG, "decode-step append needs n_tok == batch");
+    if (K.int8) return cuda_status(launch_int8_step(K, C, k, v, dtype, st), "tq_append_page");
     return cuda_status(launch_append_step(K, C, k, v, dtype, st), "tq_append_page");
   }
-  if (K.kivi && n_tok % TQ_PAGE_SIZE)
-    return fail(TQ_ERR_INVALID_ARG, "kivi: direct appends write whole pages (n_tok a multiple of 16)");
+  if ((K.kivi || K.int8) && n_tok % TQ_PAGE_SIZE)
+    return fail(TQ_ERR_INVALID_ARG, K.int8 ? "int8: direct appends write whole pages (n_tok a multiple of 16)"
+                                           : "kivi: direct appends write whole pages (n_tok a multiple of 16)");
+  if (K.int8)
+    return cuda_status(launch_int8_direct(K, C, k, v, dtype, n_tok, reinterpret_cast<const long long*>(slot_mapping), st),
+                       "tq_append_page");
   return cuda_status(launch_append_direct(K, C, k, v, dtype, n_tok, reinterpret_cast<const long long*>(slot_mapping), st),
                      "tq_append_page");
 }
@@ -295,6 +322,9 @@ extern "C" tq_status tq_prefill_cache(const tq_layer_params* p, tq_cache* cache,
   if ((n_c + TQ_PAGE_SIZE - 1) / TQ_PAGE_SIZE > cache->max_pages_per_seq)
     return fail(TQ_ERR_CAPACITY, "tq_prefill_cache: n_tok needs more pages than max_pages_per_seq");
   if ((long long)cache->batch * n_c >= (1LL << 40)) return fail(TQ_ERR_INVALID_ARG, "tq_prefill_cache: too many tokens");
+  if (K.int8)
+    return cuda_status(launch_int8_prefill_cache(K, C, k, v, dtype, n_tok, n_c, reinterpret_cast<cudaStream_t>(stream)),
+                       "tq_prefill_cache");
   return cuda_status(launch_prefill_cache(K, C, k, v, dtype, n_tok, n_c, reinterpret_cast<cudaStream_t>(stream)),
                      "tq_prefill_cache");
 }
@@ -304,7 +334,7 @@ extern "C" size_t tq_decode_workspace_size(const tq_layer_params* p, int batch, 
   if (make_params(p, &K, false) != TQ_OK || batch < 1 || max_ctx < 0 || n_splits < 0) return 0;
   if (!decode_rows_ok(K, batch)) return 0;
   clear_error();
-  return decode_ws_layout(K, batch, max_ctx, n_splits, num_sms()).total;
+  return decode_layout(K, batch, max_ctx, n_splits).total;
 }
 
 extern "C" tq_status tq_decode_attention(const tq_layer_params* p, const tq_cache* cache, const void* q, tq_dtype dtype,
@@ -321,11 +351,15 @@ extern "C" tq_status tq_decode_attention(const tq_layer_params* p, const tq_cach
   if (max_ctx < 0 || n_splits < 0) return fail(TQ_ERR_INVALID_ARG, "max_ctx and n_splits must be >= 0");
   if (!(scale == scale)) return fail(TQ_ERR_INVALID_ARG, "scale is NaN");
   if (!decode_rows_ok(K, cache->batch)) return fail(TQ_ERR_INVALID_ARG, "batch must be <= 65535 and batch * G <= 262140");
-  const WsLayout L = decode_ws_layout(K, cache->batch, max_ctx, n_splits, num_sms());
+  const WsLayout L = decode_layout(K, cache->batch, max_ctx, n_splits);
   if (workspace_bytes < L.total) {
     set_error("workspace too small: %zu < %zu", workspace_bytes, L.total);
     return TQ_ERR_CAPACITY;
   }
+  if (K.int8)
+    return cuda_status(launch_int8_decode(K, C, q, dtype, scale, nullptr, nullptr, 0, out, lse, scores, workspace, L, max_ctx,
+                                          reinterpret_cast<cudaStream_t>(stream)),
+                       "tq_decode_attention");
   return cuda_status(launch_decode(K, C, q, dtype, scale, out, lse, scores, workspace, L, max_ctx,
                                    reinterpret_cast<cudaStream_t>(stream)),
                      "tq_decode_attention");
@@ -374,6 +408,9 @@ extern "C" tq_status tq_prefill_attention(const tq_layer_params* p, const tq_cac
   V.n_compressed = nc_v;
   V.parent = parent;
   V.batch = (int)nv;
+  if (K.int8)
+    return cuda_status(launch_int8_decode(K, V, q, dtype, scale, nullptr, nullptr, 0, out, lse, nullptr, dws, L, max_ctx, st),
+                       "tq_prefill_attention");
   if (prefill_tiles_ok(K))
     return cuda_status(launch_prefill_tiles(K, V, n_query, cache->batch, q, dtype, scale, out, lse, dws, L, max_ctx, st),
                        "tq_prefill_attention");
@@ -384,15 +421,184 @@ extern "C" tq_status tq_prefill_attention(const tq_layer_params* p, const tq_cac
 extern "C" tq_status tq_check_device_error(tq_stream_t stream, uint32_t* bits_out) {
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_status(e, "tq_check_device_error: stream");
-  unsigned a = 0, b = 0;
+  unsigned a = 0, b = 0, c = 0, d = 0, f = 0;
   if ((e = read_clear_quant_error(&a)) != cudaSuccess) return cuda_status(e, "tq_check_device_error");
   if ((e = read_clear_decode_error(&b)) != cudaSuccess) return cuda_status(e, "tq_check_device_error");
-  if (bits_out) *bits_out = a | b;
-  if (a | b) {
-    set_error("device error word 0x%x", a | b);
+  if ((e = read_clear_int8_error(&c)) != cudaSuccess) return cuda_status(e, "tq_check_device_error");
+  if ((e = read_clear_int8_decode_error(&d)) != cudaSuccess) return cuda_status(e, "tq_check_device_error");
+  if ((e = read_clear_pages_error(&f)) != cudaSuccess) return cuda_status(e, "tq_check_device_error");
+  a |= b | c | d | f;
+  if (bits_out) *bits_out = a;
+  if (a) {
+    set_error("device error word 0x%x", a);
     return TQ_ERR_DEVICE_CHECK;
   }
   return ok();
+}
+
+// ------------------------------------------------------------------ 8-bit arm: values read back
+
+extern "C" tq_status tq_read_cache(const tq_layer_params* p, const tq_cache* cache, void* k, void* v, tq_dtype dtype, int first,
+                                   int n_tok, tq_stream_t stream) {
+  KParams K;
+  KCache C;
+  tq_status s = make_params(p, &K, true);
+  if (s != TQ_OK) return s;
+  if ((s = check_dtype(dtype)) != TQ_OK) return s;
+  if (!K.int8) return fail(TQ_ERR_UNSUPPORTED, "tq_read_cache: int8 layers only");
+  if ((s = make_cache(cache, K, &C, true)) != TQ_OK) return s;
+  if (first < 0 || n_tok < 0 || (long long)first + n_tok > (1LL << 31) - 64)
+    return fail(TQ_ERR_INVALID_ARG, "tq_read_cache: bad position range");
+  if (n_tok == 0) return ok();
+  if (!k || !v || !aligned(k, 16) || !aligned(v, 16)) return fail(TQ_ERR_INVALID_ARG, "k / v null or not 16-byte aligned");
+  return cuda_status(launch_int8_read(K, C, k, v, dtype, first, n_tok, reinterpret_cast<cudaStream_t>(stream)), "tq_read_cache");
+}
+
+// ------------------------------------------------------------------ page selection and attention over it
+
+static tq_status check_choice(int k, int n_sink, int n_recent, const char* what) {
+  if (k >= 1 && n_sink >= 0 && n_recent >= 0 && (long long)n_sink + n_recent <= k) return TQ_OK;
+  set_error("%s: needs a count >= 1 and n_sink, n_recent >= 0 that fit it", what);
+  return TQ_ERR_INVALID_ARG;
+}
+
+extern "C" size_t tq_select_workspace_size(const tq_layer_params* p, int batch, int max_ctx) {
+  KParams K;
+  if (make_params(p, &K, false) != TQ_OK) return 0;
+  if (!K.int8 || batch < 1 || batch > 65535 || max_ctx < 0) {
+    set_error("tq_select_workspace_size: an int8 layer, batch 1..65535 and max_ctx >= 0");
+    return 0;
+  }
+  clear_error();
+  return select_ws_bytes(K, batch, max_ctx);
+}
+
+extern "C" tq_status tq_select_pages(const tq_layer_params* p, const tq_cache* cache, const void* q, tq_dtype dtype, int n_sel,
+                                     int n_sink, int n_recent, int32_t* pages, int32_t* counts, void* workspace,
+                                     size_t workspace_bytes, int max_ctx, tq_stream_t stream) {
+  KParams K;
+  KCache C;
+  tq_status s = make_params(p, &K, true);
+  if (s != TQ_OK) return s;
+  if ((s = check_dtype(dtype)) != TQ_OK) return s;
+  if (!K.int8) return fail(TQ_ERR_UNSUPPORTED, "tq_select_pages: int8 layers only (their pages hold channel bounds)");
+  if ((s = make_cache(cache, K, &C, false)) != TQ_OK) return s;
+  if ((s = check_choice(n_sel, n_sink, n_recent, "tq_select_pages")) != TQ_OK) return s;
+  if (!q || !pages || !counts || !workspace) return fail(TQ_ERR_INVALID_ARG, "null q / pages / counts / workspace");
+  if (!aligned(workspace, 256)) return fail(TQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (max_ctx < 0) return fail(TQ_ERR_INVALID_ARG, "max_ctx must be >= 0");
+  if (!decode_rows_ok(K, cache->batch)) return fail(TQ_ERR_INVALID_ARG, "batch must be <= 65535 and batch * G <= 262140");
+  if (workspace_bytes < select_ws_bytes(K, cache->batch, max_ctx)) {
+    set_error("workspace too small: %zu < %zu", workspace_bytes, select_ws_bytes(K, cache->batch, max_ctx));
+    return TQ_ERR_CAPACITY;
+  }
+  return cuda_status(launch_select(K, C, q, dtype, n_sel, n_sink, n_recent, pages, counts, workspace, max_ctx,
+                                   reinterpret_cast<cudaStream_t>(stream)),
+                     "tq_select_pages");
+}
+
+static WsLayout pages_layout(const KParams& K, int batch, int n_sel, int n_splits) {
+  return int8_ws_layout(K, batch, (long long)n_sel + (K.window + 2 * TQ_PAGE_SIZE - 2) / TQ_PAGE_SIZE, n_splits, num_sms());
+}
+
+extern "C" size_t tq_decode_pages_workspace_size(const tq_layer_params* p, int batch, int n_sel, int n_splits) {
+  KParams K;
+  if (make_params(p, &K, false) != TQ_OK) return 0;
+  if (!K.int8 || n_sel < 1 || n_splits < 0 || !decode_rows_ok(K, batch)) {
+    set_error("tq_decode_pages_workspace_size: an int8 layer, batch as in tq_decode_attention, n_sel >= 1, n_splits >= 0");
+    return 0;
+  }
+  clear_error();
+  return pages_layout(K, batch, n_sel, n_splits).total;
+}
+
+extern "C" tq_status tq_decode_attention_pages(const tq_layer_params* p, const tq_cache* cache, const void* q, tq_dtype dtype,
+                                               float scale, const int32_t* pages, const int32_t* counts, int n_sel, float* out,
+                                               float* lse, void* workspace, size_t workspace_bytes, int max_ctx, int n_splits,
+                                               tq_stream_t stream) {
+  KParams K;
+  KCache C;
+  tq_status s = make_params(p, &K, true);
+  if (s != TQ_OK) return s;
+  if ((s = check_dtype(dtype)) != TQ_OK) return s;
+  if (!K.int8) return fail(TQ_ERR_UNSUPPORTED, "tq_decode_attention_pages: int8 layers only");
+  if ((s = make_cache(cache, K, &C, true)) != TQ_OK) return s;
+  if (!q || !out || !workspace || !pages || !counts)
+    return fail(TQ_ERR_INVALID_ARG, "null q / out / workspace / pages / counts");
+  if (!aligned(workspace, 256)) return fail(TQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (max_ctx < 0 || n_splits < 0 || n_sel < 1) return fail(TQ_ERR_INVALID_ARG, "max_ctx, n_splits >= 0 and n_sel >= 1");
+  if (!(scale == scale)) return fail(TQ_ERR_INVALID_ARG, "scale is NaN");
+  if (!decode_rows_ok(K, cache->batch)) return fail(TQ_ERR_INVALID_ARG, "batch must be <= 65535 and batch * G <= 262140");
+  const WsLayout L = pages_layout(K, cache->batch, n_sel, n_splits);
+  if (workspace_bytes < L.total) {
+    set_error("workspace too small: %zu < %zu", workspace_bytes, L.total);
+    return TQ_ERR_CAPACITY;
+  }
+  return cuda_status(launch_int8_decode(K, C, q, dtype, scale, pages, counts, n_sel, out, lse, nullptr, workspace, L, max_ctx,
+                                        reinterpret_cast<cudaStream_t>(stream)),
+                     "tq_decode_attention_pages");
+}
+
+// ------------------------------------------------------------------ eviction by attention weight
+
+extern "C" tq_status tq_track_pages(const tq_layer_params* p, const tq_cache* cache, const float* scores, const float* lse,
+                                    float* mass, int max_ctx, tq_stream_t stream) {
+  KParams K;
+  KCache C;
+  tq_status s = make_params(p, &K, false);
+  if (s != TQ_OK) return s;
+  if ((s = make_cache(cache, K, &C, false)) != TQ_OK) return s;
+  if (!scores || !lse || !mass) return fail(TQ_ERR_INVALID_ARG, "null scores / lse / mass");
+  if (max_ctx < 0 || cache->batch > 65535) return fail(TQ_ERR_INVALID_ARG, "max_ctx >= 0 and batch <= 65535");
+  if (max_ctx == 0) return ok();
+  return cuda_status(launch_track(K, C, scores, lse, mass, max_ctx, reinterpret_cast<cudaStream_t>(stream)), "tq_track_pages");
+}
+
+extern "C" size_t tq_evict_workspace_size(const tq_layer_params* p, int batch, int max_pages_per_seq) {
+  KParams K;
+  if (make_params(p, &K, false) != TQ_OK) return 0;
+  if (batch < 1 || batch > 65535 || max_pages_per_seq < 1) {
+    set_error("tq_evict_workspace_size: batch 1..65535 and max_pages_per_seq >= 1");
+    return 0;
+  }
+  clear_error();
+  return (size_t)batch * max_pages_per_seq * 2 * sizeof(int32_t);
+}
+
+extern "C" tq_status tq_evict_pages(const tq_layer_params* p, const tq_cache* cache, tq_cache* after, const float* mass,
+                                    float* mass_after, int budget, int n_sink, int n_recent, int32_t* kept, void* workspace,
+                                    size_t workspace_bytes, tq_stream_t stream) {
+  KParams K;
+  KCache A, B;
+  tq_status s = make_params(p, &K, false);
+  if (s != TQ_OK) return s;
+  if ((s = make_cache(cache, K, &A, true)) != TQ_OK) return s;
+  if ((s = make_cache(after, K, &B, true)) != TQ_OK) return s;
+  if ((s = check_choice(budget, n_sink, n_recent, "tq_evict_pages")) != TQ_OK) return s;
+  if (!mass || !mass_after || !workspace) return fail(TQ_ERR_INVALID_ARG, "null mass / mass_after / workspace");
+  if (!aligned(workspace, 256)) return fail(TQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  if (cache->batch != after->batch || cache->max_pages_per_seq != after->max_pages_per_seq || cache->batch > 65535 ||
+      cache->page_pool != after->page_pool || cache->n_pages != after->n_pages)
+    return fail(TQ_ERR_INVALID_ARG, "tq_evict_pages: the two caches must have the same pool and shape, batch <= 65535");
+  // each output buffer is either its input or another buffer; a cache is thinned in place or into one that shares nothing
+  const int same = (cache->block_table == after->block_table) + (cache->seq_len == after->seq_len) +
+                   (cache->n_compressed == after->n_compressed);
+  const bool win_same = K.window == 0 || (cache->win_k == after->win_k && cache->win_v == after->win_v);
+  const bool win_apart = K.window == 0 || (cache->win_k != after->win_k && cache->win_v != after->win_v);
+  if (!((same == 3 && win_same) || (same == 0 && win_apart)))
+    return fail(TQ_ERR_INVALID_ARG, "tq_evict_pages: `after` is the cache itself or has its own table, counters and window");
+  if (K.window > 0 && (!aligned(cache->win_k, 16) || !aligned(cache->win_v, 16) || !aligned(after->win_k, 16) || !aligned(after->win_v, 16)))
+    return fail(TQ_ERR_INVALID_ARG, "window rings must be 16-byte aligned");
+  if (same == 3 && A.ring > evict_ring_limit())
+    return fail(TQ_ERR_UNSUPPORTED, "tq_evict_pages: a window this long is moved into another cache only");
+  const size_t need = (size_t)cache->batch * cache->max_pages_per_seq * 2 * sizeof(int32_t);
+  if (workspace_bytes < need) {
+    set_error("workspace too small: %zu < %zu", workspace_bytes, need);
+    return TQ_ERR_CAPACITY;
+  }
+  return cuda_status(launch_evict(K, A, B, mass, mass_after, budget, n_sink, n_recent, kept, workspace,
+                                  reinterpret_cast<cudaStream_t>(stream)),
+                     "tq_evict_pages");
 }
 
 #ifdef TQ_TEST_HOOKS
@@ -426,7 +632,7 @@ extern "C" tq_status tq_decode_attention_static(const tq_layer_params* p, const 
   if (!cache || cache->batch < 1 || max_ctx < 0 || n_splits < 0)
     return fail(TQ_ERR_INVALID_ARG, "tq_decode_attention_static: bad cache, max_ctx or n_splits");
   if (!decode_rows_ok(K, cache->batch)) return fail(TQ_ERR_INVALID_ARG, "batch must be <= 65535 and batch * G <= 262140");
-  const size_t need = decode_ws_layout(K, cache->batch, max_ctx, n_splits, num_sms()).total;
+  const size_t need = decode_layout(K, cache->batch, max_ctx, n_splits).total;
   if (need > (size_t)TQ_STATIC_SCRATCH_BYTES) {
     set_error("tq_decode_attention_static: this configuration needs %zu bytes of scratch, more than the %u-byte "
               "static array; use tq_decode_attention with a workspace", need, (unsigned)TQ_STATIC_SCRATCH_BYTES);

@@ -42,6 +42,7 @@ struct KParams {
   // off_kcodes / off_vcodes hold the codes
   int kivi;
   int off_kscale, off_kzero, off_vscale, off_vzero;
+  int int8;                            // 8-bit arm: its page layout is in tq_int8.cuh
 };
 
 // Byte key norm ([Design study] §Packed format, u8 log-norm): 0 for a zero

@@ -1,0 +1,108 @@
+// Page format and device helpers of the 8-bit arm (sm_103a).
+//
+// A page of one KV head: 16 tokens' key codes and value codes, c + 128 in a byte with
+// c = nearest integer to x / s (ties to even), s = max |x| / 127 over the page and head, one s
+// for the keys and one for the values; and for every channel the smallest and largest key code
+// (signed), which bound the score of any query against the page.  Sub-block:
+//   int8 kmin[d], int8 kmax[d], float ks, float vs, 24 bytes 0, uint8 keys[16 d], uint8 values[16 d]
+// The codes lie in the order in which a warp's lanes take them as operands of
+// mma.m16n8k16 (lane = 4 g8 + t4), so that every load is 16 bytes a lane, 512 contiguous:
+//   keys   [nt 2][j d/64][g8 8][t4 4][16]: token 4 (g8 / 2) + 2 nt + g8 % 2, dims 64 j + 16 t4 + 0..15
+//   values [j d/64][half 2][g8 8][t4 4][i 4][s 4]: dim 64 j + 8 g8 + 4 half + i, token 4 t4 + s
+#pragma once
+
+#include "tq_device.cuh"
+
+namespace tq {
+
+constexpr int kI8Head = 32;  // bytes of scales and padding in front of the codes
+
+__host__ __device__ constexpr int i8_off_head(int d) { return 2 * d; }
+__host__ __device__ constexpr int i8_off_kcodes(int d) { return 2 * d + kI8Head; }
+__host__ __device__ constexpr int i8_off_vcodes(int d) { return 18 * d + kI8Head; }
+__host__ __device__ constexpr int i8_sub_bytes(int d) { return 34 * d + kI8Head; }
+
+__device__ __forceinline__ unsigned char* i8_subblock(const KParams& P, const KCache& C, long long page, int head) {
+  return C.pool + ((size_t)page * P.hkv + head) * (size_t)P.sub_bytes;
+}
+
+// Page scale of a largest magnitude: float32 quotient; below the normal range the page is all zero codes.
+__device__ __forceinline__ float i8_scale(float amax) {
+  const float s = __fdiv_rn(amax, 127.f);
+  return s < 1.17549435e-38f ? 0.f : s;
+}
+// |x| where x is finite, else 0 (non-finite entries do not set the scale)
+__device__ __forceinline__ float i8_mag(float x) {
+  const float a = fabsf(x);
+  return a <= 3.402823466e38f ? a : 0.f;
+}
+
+// Nearest code where the fast path cannot tell: half steps (to even), and what is not finite
+// (NaN 0, infinities the largest code).  c is within 1 of x / s.
+static __device__ __noinline__ float i8_code_slow(float x, float s, float c) {
+  if (!(fabsf(x) <= 3.402823466e38f)) return x != x || s == 0.f ? 0.f : copysignf(127.f, x);
+  if (s == 0.f) return 0.f;
+  const float r = fmaf(-c, s, x), h = 0.5f * s;
+  if (fabsf(r) > h || (fabsf(r) == h && (((int)c) & 1))) c += copysignf(1.f, r);
+  return fminf(fmaxf(c, -127.f), 127.f);
+}
+
+// Code + 128 of x at scale s, inv = 1 / s (0 where s is 0), in the low byte of the result.
+// x inv + 1.5 2^23 rounds to an integer whose low byte is the code; it is the nearest to the
+// exact quotient unless the residual x - c s (exact in float: a multiple of half an ulp of s
+// below 2^24 of them) reaches half a step.
+__device__ __forceinline__ uint32_t i8_code(float x, float s, float inv) {
+  constexpr float kMagic = 12582912.f;  // 1.5 * 2^23
+  const float m = fmaf(x, inv, kMagic);
+  float c = m - kMagic;
+  const float r = fmaf(-c, s, x);
+  uint32_t bits = __float_as_uint(m) + 128u;
+  if (!(fabsf(r) < 0.5f * s)) {
+    c = i8_code_slow(x, s, c);
+    bits = (uint32_t)((int)c + 128);
+  }
+  return bits;
+}
+
+// Low bytes of four words as one word.
+__device__ __forceinline__ uint32_t i8_pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  uint32_t lo, hi, r;
+  asm("prmt.b32 %0, %1, %2, 0x0040;" : "=r"(lo) : "r"(a), "r"(b));
+  asm("prmt.b32 %0, %1, %2, 0x0040;" : "=r"(hi) : "r"(c), "r"(d));
+  asm("prmt.b32 %0, %1, %2, 0x5410;" : "=r"(r) : "r"(lo), "r"(hi));
+  return r;
+}
+
+// Two code bytes (0, 1 or 2, 3 of w) as an f16 pair, exact: 1024 + u read off the bits, minus 1152.
+__device__ __forceinline__ uint32_t i8_lo2(uint32_t w) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, 0x4140;" : "=r"(r) : "r"(w), "r"(0x64646464u));
+  __half2 h = __hsub2(*reinterpret_cast<__half2*>(&r), __half2half2(__ushort_as_half(0x6480)));
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t i8_hi2(uint32_t w) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, %2, 0x4342;" : "=r"(r) : "r"(w), "r"(0x64646464u));
+  __half2 h = __hsub2(*reinterpret_cast<__half2*>(&r), __half2half2(__ushort_as_half(0x6480)));
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+// Elements 2 i, 2 i + 1 of a 16-byte piece (bf16 or f16), or i of four floats.
+template <typename T>
+__device__ __forceinline__ float elem_of(const uint4& w, int i);
+template <>
+__device__ __forceinline__ float elem_of<float>(const uint4& w, int i) {
+  return __uint_as_float(i == 0 ? w.x : i == 1 ? w.y : i == 2 ? w.z : w.w);
+}
+template <>
+__device__ __forceinline__ float elem_of<__nv_bfloat16>(const uint4& w, int i) {
+  const uint32_t u = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
+  return __uint_as_float(i & 1 ? u & 0xffff0000u : u << 16);
+}
+template <>
+__device__ __forceinline__ float elem_of<__half>(const uint4& w, int i) {
+  const uint32_t u = i < 2 ? w.x : i < 4 ? w.y : i < 6 ? w.z : w.w;
+  return __half2float(__ushort_as_half((unsigned short)(i & 1 ? u >> 16 : u & 0xffffu)));
+}
+
+}  // namespace tq

@@ -1,0 +1,438 @@
+// Writing and reading the pages of the 8-bit arm (format: tq_int8.cuh).
+//
+// One warp quantizes one page of one head, keys or values: its lanes load the 16 tokens' rows in
+// the pieces whose codes they store (keys: 16 dims of a token, values: 8 dims of four tokens), keep
+// them in registers, agree on the largest magnitude with shuffles, and write the codes 16 bytes a lane,
+// 512 contiguous.  Every element is read once and no shared memory is used; what bounds the kernel is
+// the traffic (2 or 4 bytes in and 1 out an element).
+#include <algorithm>
+#include <type_traits>
+
+#include "tq_int8.cuh"
+#include "tq_launch.h"
+
+namespace tq {
+
+static __device__ unsigned int g_int8_err = 0;
+
+namespace {
+
+constexpr int kWriteWarps = 4;
+
+// Byte-wise signed minimum / maximum over the lanes with the same t4 (lane bits 2..4).
+__device__ __forceinline__ uint32_t min_over_g8(uint32_t v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v = __vmins4(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ uint32_t max_over_g8(uint32_t v) {
+#pragma unroll
+  for (int o = 4; o < 32; o <<= 1) v = __vmaxs4(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// Quantizes 16 tokens of one head into sub-block sb; row(t) is token t's row of dh elements of type T
+// (16-byte aligned), dims dh .. D-1 are zero.
+template <int D, typename T, typename Row>
+__device__ __forceinline__ void i8_write_page(Row row, int dh, bool is_key, unsigned char* sb) {
+  constexpr int EPL = 16 / (int)sizeof(T);  // elements of a 16-byte load
+  constexpr int J = D / 64;
+  const int lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  if (is_key) {
+    constexpr int L = 16 / EPL;
+    uint4 raw[2][J][L];
+    float a = 0.f;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt) {
+      const T* r = row(4 * (g8 >> 1) + 2 * nt + (g8 & 1));
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int l = 0; l < L; ++l) {
+          const int c = 64 * j + 16 * t4 + l * EPL;  // dh is a multiple of 8, so a piece is in or out
+          raw[nt][j][l] = c < dh ? *reinterpret_cast<const uint4*>(r + c) : zero;
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int l = 0; l < L; ++l)
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) a = fmaxf(a, i8_mag(elem_of<T>(raw[nt][j][l], e)));
+    const float s = i8_scale(warp_max_f(a)), inv = s > 0.f ? __frcp_rn(s) : 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j) {
+      uint32_t mn[4], mx[4];
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t u[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            u[e] = i8_code(elem_of<T>(raw[nt][j][(4 * i + e) / EPL], (4 * i + e) % EPL), s, inv);
+          w[i] = i8_pack4(u[0], u[1], u[2], u[3]);
+          const uint32_t sc = w[i] ^ 0x80808080u;  // signed codes
+          mn[i] = nt == 0 ? sc : __vmins4(mn[i], sc);
+          mx[i] = nt == 0 ? sc : __vmaxs4(mx[i], sc);
+        }
+        *reinterpret_cast<uint4*>(sb + i8_off_kcodes(D) + nt * 8 * D + j * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        mn[i] = min_over_g8(mn[i]);
+        mx[i] = max_over_g8(mx[i]);
+      }
+      if (g8 == 0) *reinterpret_cast<uint4*>(sb + 64 * j + 16 * t4) = make_uint4(mn[0], mn[1], mn[2], mn[3]);
+      if (g8 == 1) *reinterpret_cast<uint4*>(sb + D + 64 * j + 16 * t4) = make_uint4(mx[0], mx[1], mx[2], mx[3]);
+    }
+    if (lane == 0) *reinterpret_cast<float*>(sb + i8_off_head(D)) = s;
+    if (lane >= 2 && lane < 8) *reinterpret_cast<float*>(sb + i8_off_head(D) + 4 * lane) = 0.f;  // the padding
+  } else {
+    constexpr int L = 8 / EPL;
+    uint4 raw[J][4][L];
+    float a = 0.f;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const T* r = row(4 * t4 + t);
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int l = 0; l < L; ++l) {
+          const int c = 64 * j + 8 * g8 + l * EPL;
+          raw[j][t][l] = c < dh ? *reinterpret_cast<const uint4*>(r + c) : zero;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int l = 0; l < L; ++l)
+#pragma unroll
+          for (int e = 0; e < EPL; ++e) a = fmaxf(a, i8_mag(elem_of<T>(raw[j][t][l], e)));
+    const float s = i8_scale(warp_max_f(a)), inv = s > 0.f ? __frcp_rn(s) : 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t u[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+            u[t] = i8_code(elem_of<T>(raw[j][t][(4 * half + i) / EPL], (4 * half + i) % EPL), s, inv);
+          w[i] = i8_pack4(u[0], u[1], u[2], u[3]);
+        }
+        *reinterpret_cast<uint4*>(sb + i8_off_vcodes(D) + j * 1024 + half * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    if (lane == 0) *reinterpret_cast<float*>(sb + i8_off_head(D) + 4) = s;
+  }
+}
+
+// One row into the float16 ring (zero tail past dh), one warp.
+template <int D, typename T>
+__device__ __forceinline__ void i8_window_row(const T* src, int dh, __half* dst) {
+  const int lane = threadIdx.x & 31;
+  for (int c = 4 * lane; c < D; c += 128) {  // dh is a multiple of 8: four dims are in or out
+    __half h[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float x = 0.f;
+      if (c < dh) {
+        if constexpr (sizeof(T) == 4) x = reinterpret_cast<const float*>(src)[c + e];
+        else x = (float)src[c + e];
+      }
+      h[e] = __float2half_rn(x);
+    }
+    *reinterpret_cast<uint2*>(dst + c) = *reinterpret_cast<const uint2*>(h);
+  }
+}
+
+// Whole sequences: tasks 0 .. batch (n_c / 16) 2 hkv - 1 are pages (heads fastest, so that
+// neighbouring warps read neighbouring rows), then one task per window row; thread 0 of block b sets
+// sequence b's counters.
+template <int D, typename T>
+__global__ void __launch_bounds__(32 * kWriteWarps) i8_prefill_kernel(const __grid_constant__ KParams P,
+                                                                      const __grid_constant__ KCache C, const T* k,
+                                                                      const T* v, int n_tok, int n_c) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long gid = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  for (long long b = gid; b < C.batch; b += (long long)gridDim.x * blockDim.x) {
+    C.seq_len[b] = n_tok;
+    C.n_compressed[b] = n_c;
+  }
+  const int np = n_c / kPage, rows = n_tok - n_c;
+  const long long pages = (long long)C.batch * np * 2 * P.hkv;
+  const long long tasks = pages + (long long)C.batch * rows * 2 * P.hkv;
+  for (long long t = (long long)blockIdx.x * kWriteWarps + warp; t < tasks; t += (long long)gridDim.x * kWriteWarps) {
+    const bool is_page = t < pages;
+    long long u = is_page ? t : t - pages;
+    const int head = (int)(u % P.hkv);
+    u /= P.hkv;
+    const bool is_key = (u & 1) == 0;
+    u >>= 1;
+    const T* x = is_key ? k : v;
+    if (is_page) {
+      const int b = (int)(u / np), pg = (int)(u % np);
+      const long long page = C.block_table[(size_t)b * C.max_pages + pg];
+      if (page < 0 || page >= C.n_pages) {
+        if (lane == 0) atomicOr(&g_int8_err, TQ_DEVERR_SLOT);
+        continue;
+      }
+      const T* x0 = x + (((size_t)b * n_tok + (size_t)pg * kPage) * P.hkv + head) * P.dh;
+      const size_t stride = (size_t)P.hkv * P.dh;
+      i8_write_page<D, T>([&](int i) { return x0 + i * stride; }, P.dh, is_key, i8_subblock(P, C, page, head));
+    } else {
+      const int b = (int)(u / rows), p = n_c + (int)(u % rows);
+      i8_window_row<D, T>(x + (((size_t)b * n_tok + p) * P.hkv + head) * P.dh, P.dh,
+                          (is_key ? C.win_k : C.win_v) + (((size_t)b * P.hkv + head) * C.ring + p % C.ring) * D);
+    }
+  }
+}
+
+// Direct slots: 16 consecutive tokens fill one page in order, or are all skipped (negative slots).
+template <int D, typename T>
+__global__ void __launch_bounds__(32 * kWriteWarps) i8_direct_kernel(const __grid_constant__ KParams P,
+                                                                     const __grid_constant__ KCache C, const T* k,
+                                                                     const T* v, long long n_tok, const long long* slots) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long tasks = n_tok / kPage * 2 * P.hkv;
+  for (long long t = (long long)blockIdx.x * kWriteWarps + warp; t < tasks; t += (long long)gridDim.x * kWriteWarps) {
+    const int head = (int)(t % P.hkv);
+    const bool is_key = (t / P.hkv & 1) == 0;
+    const long long t0 = t / (2 * P.hkv) * kPage;
+    const long long mine = slots[t0 + (lane & 15)], first = __shfl_sync(0xffffffffu, mine, 0);
+    if (__all_sync(0xffffffffu, mine < 0)) continue;
+    const long long page = first / kPage;
+    const bool good = first >= 0 && mine == page * kPage + (lane & 15) && page < C.n_pages;
+    if (!__all_sync(0xffffffffu, good)) {
+      if (lane == 0) atomicOr(&g_int8_err, TQ_DEVERR_SLOT);
+      continue;
+    }
+    const T* x0 = (is_key ? k : v) + ((size_t)t0 * P.hkv + head) * P.dh;
+    const size_t stride = (size_t)P.hkv * P.dh;
+    i8_write_page<D, T>([&](int i) { return x0 + i * stride; }, P.dh, is_key, i8_subblock(P, C, page, head));
+  }
+}
+
+constexpr int kStepWarps = 8;
+
+// Decode step, one block a sequence: every head's row into the ring; where the window then holds
+// W + 16 tokens its oldest 16 (never the new one: W >= 1) become a page.  The block advances the
+// sequence's counters when all of its warps have read them.
+template <int D, typename T>
+__global__ void __launch_bounds__(32 * kStepWarps) i8_step_kernel(const __grid_constant__ KParams P,
+                                                                  const __grid_constant__ KCache C, const T* k, const T* v) {
+  const int b = blockIdx.x, warp = threadIdx.x >> 5;
+  const int n = C.seq_len[b], nc = C.n_compressed[b];
+  if (nc < 0 || n - nc < 0 || n - nc >= P.window + kPage) {
+    if (threadIdx.x == 0) atomicOr(&g_int8_err, TQ_DEVERR_SEQ_LEN);
+    return;
+  }
+  const bool flush = n + 1 - nc == P.window + kPage;
+  const int pidx = nc / kPage;
+  long long page = -1;
+  if (flush) {
+    if (pidx < C.max_pages) page = C.block_table[(size_t)b * C.max_pages + pidx];
+    if (page < 0 || page >= C.n_pages) {
+      // no page to flush into: the step is not taken, so that no token is lost from the window
+      if (threadIdx.x == 0) atomicOr(&g_int8_err, pidx < C.max_pages ? TQ_DEVERR_PAGE_INDEX : TQ_DEVERR_SEQ_LEN);
+      return;
+    }
+  }
+  for (int t = warp; t < 2 * P.hkv; t += kStepWarps) {
+    const int head = t >> 1;
+    const bool is_key = (t & 1) == 0;
+    __half* ring = (is_key ? C.win_k : C.win_v) + (((size_t)b * P.hkv + head) * C.ring) * D;
+    i8_window_row<D, T>((is_key ? k : v) + ((size_t)b * P.hkv + head) * P.dh, P.dh, ring + (size_t)(n % C.ring) * D);
+    if (flush)
+      i8_write_page<D, __half>([&](int i) { return ring + (size_t)((nc + i) % C.ring) * D; }, D, is_key,
+                               i8_subblock(P, C, page, head));
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    C.seq_len[b] = n + 1;
+    if (flush) C.n_compressed[b] = nc + kPage;
+  }
+}
+
+// N values to N adjacent outputs (16-byte stores; N times the size of T a multiple of 16).
+template <typename T, int N>
+__device__ __forceinline__ void store_row(T* p, const float (&x)[N]) {
+  uint32_t w[N * sizeof(T) / 4];
+#pragma unroll
+  for (int i = 0; i < (int)(N * sizeof(T) / 4); ++i) {
+    if constexpr (sizeof(T) == 4) {
+      w[i] = __float_as_uint(x[i]);
+    } else {
+      T a, c;
+      if constexpr (std::is_same<T, __half>::value) a = __float2half_rn(x[2 * i]), c = __float2half_rn(x[2 * i + 1]);
+      else a = __float2bfloat16_rn(x[2 * i]), c = __float2bfloat16_rn(x[2 * i + 1]);
+      w[i] = (uint32_t) * reinterpret_cast<unsigned short*>(&a) | (uint32_t) * reinterpret_cast<unsigned short*>(&c) << 16;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < (int)(N * sizeof(T) / 16); ++i)
+    reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+}
+
+// The values that positions first .. first + n_tok - 1 stand for.  One warp a page of one head
+// (position / 16 counted from the sequence's start, pages and window alike), keys or values; rows of
+// positions the sequence does not have are left as they were.
+template <int D, typename T>
+__global__ void __launch_bounds__(32 * kWriteWarps) i8_read_kernel(const __grid_constant__ KParams P,
+                                                                   const __grid_constant__ KCache C, T* k, T* v, int first,
+                                                                   int n_tok) {
+  constexpr int J = D / 64;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
+  const int p0 = first / kPage, np = (int)(((long long)first + n_tok + kPage - 1) / kPage) - p0;
+  const long long tasks = (long long)C.batch * np * 2 * P.hkv;
+  for (long long t = (long long)blockIdx.x * kWriteWarps + warp; t < tasks; t += (long long)gridDim.x * kWriteWarps) {
+    long long u = t;
+    const int head = (int)(u % P.hkv);
+    u /= P.hkv;
+    const bool is_key = (u & 1) == 0;
+    u >>= 1;
+    const int b = (int)(u / np), pg = p0 + (int)(u % np);
+    const int n = C.seq_len[b], nc = C.n_compressed[b];
+    if (nc < 0 || n < nc || n - nc >= C.ring) {
+      if (lane == 0) atomicOr(&g_int8_err, TQ_DEVERR_SEQ_LEN);
+      continue;
+    }
+    const int lo = max(first, pg * kPage), hi = (int)min((long long)first + n_tok, min((long long)n, (long long)(pg + 1) * kPage));
+    if (lo >= hi) continue;
+    T* dst = (is_key ? k : v) + (((long long)b * n_tok - first) * P.hkv + head) * P.dh;  // + position * hkv * dh
+    const size_t stride = (size_t)P.hkv * P.dh;
+    if (pg * kPage < nc) {
+      const long long page = pg < C.max_pages ? C.block_table[(size_t)b * C.max_pages + pg] : -1;
+      if (page < 0 || page >= C.n_pages) {
+        if (lane == 0) atomicOr(&g_int8_err, pg < C.max_pages ? TQ_DEVERR_PAGE_INDEX : TQ_DEVERR_SEQ_LEN);
+        continue;
+      }
+      const unsigned char* sb = i8_subblock(P, C, page, head);
+      const float s = *reinterpret_cast<const float*>(sb + i8_off_head(D) + (is_key ? 0 : 4));
+      if (is_key) {
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt) {
+          const int pos = pg * kPage + 4 * (g8 >> 1) + 2 * nt + (g8 & 1);
+#pragma unroll
+          for (int j = 0; j < J; ++j) {
+            const uint4 w = *reinterpret_cast<const uint4*>(sb + i8_off_kcodes(D) + nt * 8 * D + j * 512 + lane * 16);
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+            float x[2][8];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e / 8][e % 8] = (float)((int)((ww[e / 4] >> 8 * (e % 4)) & 255u) - 128) * s;
+            const int c = 64 * j + 16 * t4;
+            if (pos >= lo && pos < hi) {
+              if (c < P.dh) store_row<T>(dst + pos * stride + c, x[0]);
+              if (c + 8 < P.dh) store_row<T>(dst + pos * stride + c + 8, x[1]);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          uint32_t ww[8];
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint4 w = *reinterpret_cast<const uint4*>(sb + i8_off_vcodes(D) + j * 1024 + half * 512 + lane * 16);
+            ww[4 * half] = w.x, ww[4 * half + 1] = w.y, ww[4 * half + 2] = w.z, ww[4 * half + 3] = w.w;
+          }
+          const int c = 64 * j + 8 * g8;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int pos = pg * kPage + 4 * t4 + i;
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = (float)((int)((ww[e] >> 8 * i) & 255u) - 128) * s;
+            if (pos >= lo && pos < hi && c < P.dh) store_row<T>(dst + pos * stride + c, x);
+          }
+        }
+      }
+    } else {
+      const __half* ring = (is_key ? C.win_k : C.win_v) + (((size_t)b * P.hkv + head) * C.ring) * D;
+      for (int i = lane; i < (hi - lo) * (D / 8); i += 32) {
+        const int pos = lo + i / (D / 8), c = i % (D / 8) * 8;
+        if (c >= P.dh) continue;
+        const uint4 w = *reinterpret_cast<const uint4*>(ring + (size_t)(pos % C.ring) * D + c);
+        float x[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = elem_of<__half>(w, e);
+        store_row<T>(dst + pos * stride + c, x);
+      }
+    }
+  }
+}
+
+// Blocks for `tasks` warps' worth of work: all of it where it fits a grid, else a strided loop.
+unsigned blocks_for(long long tasks) {
+  return (unsigned)std::max(1LL, std::min((tasks + kWriteWarps - 1) / kWriteWarps, 1LL << 30));
+}
+
+template <int D, typename T>
+cudaError_t prefill(const KParams& P, const KCache& C, const void* k, const void* v, int n_tok, int n_c, cudaStream_t st) {
+  const long long tasks = ((long long)C.batch * (n_c / kPage) + (long long)C.batch * (n_tok - n_c)) * 2 * P.hkv;
+  i8_prefill_kernel<D, T><<<blocks_for(tasks), 32 * kWriteWarps, 0, st>>>(P, C, (const T*)k, (const T*)v, n_tok, n_c);
+  return cudaGetLastError();
+}
+template <int D, typename T>
+cudaError_t direct(const KParams& P, const KCache& C, const void* k, const void* v, long long n_tok, const long long* slots,
+                   cudaStream_t st) {
+  i8_direct_kernel<D, T><<<blocks_for(n_tok / kPage * 2 * P.hkv), 32 * kWriteWarps, 0, st>>>(P, C, (const T*)k, (const T*)v,
+                                                                                             n_tok, slots);
+  return cudaGetLastError();
+}
+template <int D, typename T>
+cudaError_t step(const KParams& P, const KCache& C, const void* k, const void* v, cudaStream_t st) {
+  i8_step_kernel<D, T><<<C.batch, 32 * std::min(kStepWarps, 2 * P.hkv), 0, st>>>(P, C, (const T*)k, (const T*)v);
+  return cudaGetLastError();
+}
+template <int D, typename T>
+cudaError_t read(const KParams& P, const KCache& C, void* k, void* v, int first, int n_tok, cudaStream_t st) {
+  const long long np = ((long long)first + n_tok + kPage - 1) / kPage - first / kPage;
+  i8_read_kernel<D, T><<<blocks_for((long long)C.batch * np * 2 * P.hkv), 32 * kWriteWarps, 0, st>>>(P, C, (T*)k, (T*)v, first,
+                                                                                                   n_tok);
+  return cudaGetLastError();
+}
+
+// F<D, T>(args...) for the layer's d and the tensors' type
+#define TQ_I8_DISPATCH(F, ...)                                                              \
+  (P.d == 128 ? (dtype == TQ_F32    ? F<128, float>(__VA_ARGS__)                            \
+                 : dtype == TQ_BF16 ? F<128, __nv_bfloat16>(__VA_ARGS__)                    \
+                                    : F<128, __half>(__VA_ARGS__))                          \
+              : (dtype == TQ_F32    ? F<256, float>(__VA_ARGS__)                            \
+                 : dtype == TQ_BF16 ? F<256, __nv_bfloat16>(__VA_ARGS__)                    \
+                                    : F<256, __half>(__VA_ARGS__)))
+
+}  // namespace
+
+cudaError_t launch_int8_prefill_cache(const KParams& P, const KCache& C, const void* k, const void* v, int dtype, int n_tok,
+                                      int n_c, cudaStream_t st) {
+  return TQ_I8_DISPATCH(prefill, P, C, k, v, n_tok, n_c, st);
+}
+cudaError_t launch_int8_direct(const KParams& P, const KCache& C, const void* k, const void* v, int dtype, long long n_tok,
+                               const long long* slots, cudaStream_t st) {
+  return TQ_I8_DISPATCH(direct, P, C, k, v, n_tok, slots, st);
+}
+cudaError_t launch_int8_step(const KParams& P, const KCache& C, const void* k, const void* v, int dtype, cudaStream_t st) {
+  return TQ_I8_DISPATCH(step, P, C, k, v, st);
+}
+cudaError_t launch_int8_read(const KParams& P, const KCache& C, void* k, void* v, int dtype, int first, int n_tok,
+                             cudaStream_t st) {
+  return TQ_I8_DISPATCH(read, P, C, k, v, first, n_tok, st);
+}
+
+cudaError_t read_clear_int8_error(unsigned* bits) {
+  unsigned zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(bits, g_int8_err, sizeof(unsigned));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_int8_err, &zero, sizeof(unsigned));
+}
+
+}  // namespace tq

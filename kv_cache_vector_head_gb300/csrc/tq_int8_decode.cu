@@ -1,0 +1,434 @@
+// Decode attention over the pages of the 8-bit arm (format: tq_int8.cuh).
+//
+//   l_t = scale ks <q, c_t> (pages), scale <q, k_t> (float16 window);  out = sum_t p_t vs cv_t / sum_t p_t.
+//
+// The G <= 8 query heads of a KV head share every load.  Both products run on mma.m16n8k16 with
+// operands exact in f16: the codes as they are (integers up to 127), the query and the softmax weights
+// as f16 hi + lo limbs in rows h and h + 8 of the 16-row tile (22 bits; a single f16 limb would leave
+// 2^-12 of the float output, and with G <= 8 the second limb fills rows that were empty).  A query row is
+// scaled by a power of two so that its limbs keep clear of f16's subnormals; the pages' value scales
+// ride on the weights relative to a power of two that bounds the scales seen so far, adjusted with
+// the running maximum.
+//
+// The page holds its codes in operand order, so a lane's 16-byte load is four operands and the
+// scores come out of the first product in the layout the second one takes them: a warp carries a page
+// from load to accumulator in registers, without shared memory and without another warp.  Warps take
+// the pages (16 tokens; the window in groups of 16) of their split in turn and meet once at the end.
+#include <math.h>
+
+#include <algorithm>
+
+#include "tq_int8.cuh"
+#include "tq_launch.h"
+
+namespace tq {
+
+static __device__ unsigned int g_int8_decode_err = 0;
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kWeightTop = 16384.f;  // f16 weights reach up to this: lo limbs stay normal down to 2^-26 of the top
+
+__host__ __device__ constexpr int ctas_per_sm(int d) { return d == 128 ? 3 : 2; }
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+// f16 pair of (a, b) and of what it leaves
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(a, b);
+  const float2 f = __half22float2(h);
+  const __half2 l = __floats2half2_rn(a - f.x, b - f.y);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
+// Smallest power of two >= s (s a page scale: 0 or normal)
+__device__ __forceinline__ float pow2_above(float s) {
+  return __uint_as_float((__float_as_uint(s) + 0x007fffffu) & 0x7f800000u);
+}
+
+// 1 / v for a power of two v between 2^-126 and 2^126
+__device__ __forceinline__ float pow2_inv(float v) { return __uint_as_float(0x7f000000u - __float_as_uint(v)); }
+
+struct Shared {
+  uint4 afr[16][32];      // query operand: k-step, lane
+  float unscale[8];       // 1 / the power of two of a query row
+  float m[kWarps][8], l[kWarps][8];
+};
+
+// Row scale (a power of two that brings the largest magnitude into [2^13, 2^14)) and operand fragments of
+// the G query rows at q [G][dh].  All threads; ends with a barrier.
+template <int D>
+__device__ void load_query(Shared& sh, const void* q, int dtype, size_t row0, int G, int dh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int h = warp; h < 8; h += kWarps) {
+    float a = 0.f;
+    if (h < G)
+      for (int j = lane; j < dh; j += 32) a = fmaxf(a, i8_mag(load_elem(q, dtype, (long long)((row0 + h) * dh + j))));
+    a = warp_max_f(a);
+    // 2^(13 - floor(log2 a)); the exponent is kept where both it and its reciprocal are normal
+    const int e = a > 0.f ? min(max(140 - (int)(__float_as_uint(a) >> 23), -113), 126) : 0;
+    if (lane == 0) {
+      sh.unscale[h] = __uint_as_float((uint32_t)(127 - e) << 23);
+      sh.m[0][h] = __uint_as_float((uint32_t)(127 + e) << 23);
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < D / 16 * 32; i += kThreads) {
+    const int kk = i >> 5, ln = i & 31, h = ln >> 2, c = 64 * (kk >> 2) + 16 * (ln & 3) + 4 * (kk & 3);
+    uint4 f = make_uint4(0, 0, 0, 0);
+    if (h < G && c < dh) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = load_elem(q, dtype, (long long)((row0 + h) * dh + c + e)) * sh.m[0][h];
+      split2(x[0], x[1], f.x, f.y);
+      split2(x[2], x[3], f.z, f.w);
+    }
+    sh.afr[kk][ln] = f;
+  }
+  __syncthreads();
+}
+
+// Work of one (sequence, KV head): pages first, then the window in groups of 16.
+struct Items {
+  int n, nc, pages, total;
+  const int32_t* list;  // page ordinals to take, or null: all pages in order
+};
+
+template <int D>
+__global__ void __launch_bounds__(kThreads) i8_decode_kernel(const __grid_constant__ KParams P,
+                                                             const __grid_constant__ KCache C, const void* q, int dtype,
+                                                             float scale, const int32_t* __restrict__ pages,
+                                                             const int32_t* __restrict__ counts, int n_sel, float* out,
+                                                             float* lse, float* scores, unsigned char* ws, WsLayout L,
+                                                             int max_ctx) {
+  constexpr int J = D / 64;
+  __shared__ Shared sh;
+  extern __shared__ __align__(16) float merge[];  // [kWarps][8][D]
+  const int s = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
+  const int G = P.G, S = L.n_comp_splits;
+  const size_t head0 = (size_t)b * P.hq + (size_t)g * G;
+  const int cb = C.parent ? C.parent[b] : b;
+
+  Items it;
+  it.n = C.seq_len[b];
+  it.nc = C.n_compressed[b];
+  bool bad = false;
+  if (it.n < 0 || it.n > max_ctx || it.nc < 0 || it.nc > it.n) {
+    bad = true;
+    it.n = min(max(it.n, 0), max_ctx);
+    it.nc = min(max(it.nc, 0), it.n);
+  }
+  int np = (it.nc + kPage - 1) / kPage;
+  if (np > C.max_pages) {
+    bad = true;
+    np = C.max_pages;
+  }
+  int nwin = it.n - it.nc;
+  // positions from nc on are in the ring; a virtual sequence's nc is its parent's clipped to what it sees
+  if (nwin >= C.ring) {
+    bad = true;
+    nwin = C.ring - 1;
+  }
+  it.pages = np;
+  it.list = nullptr;
+  if (pages) {
+    it.list = pages + ((size_t)b * P.hkv + g) * n_sel;
+    it.pages = counts[(size_t)b * P.hkv + g];
+    if (it.pages < 0 || it.pages > n_sel) {
+      bad = true;
+      it.pages = min(max(it.pages, 0), n_sel);
+    }
+  }
+  if (bad && tid == 0) atomicOr(&g_int8_decode_err, TQ_DEVERR_SEQ_LEN);
+  it.total = it.pages + (nwin + kPage - 1) / kPage;
+  // the split's share, in whole rounds of the warps where there are enough
+  const int per = (it.total + S - 1) / S;
+  const int i0 = min(it.total, s * per), i1 = min(it.total, i0 + per);
+
+  load_query<D>(sh, q, dtype, head0, G, P.dh);
+  const float qs = sh.unscale[g8] * scale;
+
+  float acc[J][2][4][4];
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[j][h][i][r] = 0.f;
+  float m = -INFINITY, l = 0.f, vref = 0.f;  // of head g8 (l: this lane's tokens)
+
+  for (int i = i0 + warp; i < i1; i += kWarps) {
+    const bool is_page = i < it.pages;
+    float sacc[2][4] = {};
+    float ks = 1.f, vs = 1.f;
+    int pos0, live_to;  // position of the group's first token; tokens at positions < live_to count
+    const unsigned char* sb = nullptr;
+    if (is_page) {
+      const int ord = it.list ? it.list[i] : i;
+      long long page = -1;
+      if (ord >= 0 && ord < np) page = C.block_table[(size_t)cb * C.max_pages + ord];
+      if (page < 0 || page >= C.n_pages) {
+        if (lane == 0) atomicOr(&g_int8_decode_err, TQ_DEVERR_PAGE_INDEX);
+        continue;
+      }
+      sb = i8_subblock(P, C, page, g);
+      pos0 = ord * kPage;
+      live_to = it.nc;
+      const float2 sc = *reinterpret_cast<const float2*>(sb + i8_off_head(D));
+      ks = sc.x;
+      vs = sc.y;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const uint4 w = *reinterpret_cast<const uint4*>(sb + i8_off_kcodes(D) + nt * 8 * D + j * 512 + lane * 16);
+          mma16816(sacc[nt], sh.afr[4 * j][lane], i8_lo2(w.x), i8_hi2(w.x));
+          mma16816(sacc[nt], sh.afr[4 * j + 1][lane], i8_lo2(w.y), i8_hi2(w.y));
+          mma16816(sacc[nt], sh.afr[4 * j + 2][lane], i8_lo2(w.z), i8_hi2(w.z));
+          mma16816(sacc[nt], sh.afr[4 * j + 3][lane], i8_lo2(w.w), i8_hi2(w.w));
+        }
+    } else {
+      pos0 = it.nc + (i - it.pages) * kPage;
+      live_to = it.nc + nwin;
+      const __half* ring = C.win_k + ((size_t)cb * P.hkv + g) * C.ring * D;
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const int pos = pos0 + 4 * (g8 >> 1) + 2 * nt + (g8 & 1);
+        const __half* row = ring + (size_t)(pos % C.ring) * D + 16 * t4;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;  // rows that are not there may hold anything
+          if (pos < live_to) {
+            w0 = *reinterpret_cast<const uint4*>(row + 64 * j);
+            w1 = *reinterpret_cast<const uint4*>(row + 64 * j + 8);
+          }
+          mma16816(sacc[nt], sh.afr[4 * j][lane], w0.x, w0.y);
+          mma16816(sacc[nt], sh.afr[4 * j + 1][lane], w0.z, w0.w);
+          mma16816(sacc[nt], sh.afr[4 * j + 2][lane], w1.x, w1.y);
+          mma16816(sacc[nt], sh.afr[4 * j + 3][lane], w1.z, w1.w);
+        }
+      }
+    }
+    // scores of head g8, tokens 4 t4 + 2 nt + e
+    float x[2][2], mx = -INFINITY;
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int pos = pos0 + 4 * t4 + 2 * nt + e;
+        const float lg = (sacc[nt][e] + sacc[nt][e + 2]) * (qs * ks);
+        x[nt][e] = pos < live_to ? lg : -INFINITY;
+        mx = fmaxf(mx, x[nt][e]);
+        if (scores && g8 < G && pos < live_to) scores[(head0 + g8) * (size_t)max_ctx + pos] = lg;
+      }
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    const float mn = fmaxf(m, mx);
+    const float vn = fmaxf(vref, pow2_above(vs));
+    // a score that is NaN leaves mn as it was and makes its weights NaN
+    const float mb = mn == -INFINITY ? 0.f : mn;
+    const float al = exp2f((m - mb) * kLog2e);  // 0 before the first score
+    const float av = vn > 0.f ? al * (vref * pow2_inv(vn)) : al;
+    const float wv = vn > 0.f ? vs * pow2_inv(vn) * kWeightTop : 0.f;
+    m = mn;
+    vref = vn;
+    l *= al;
+    float p[2][2];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        p[nt][e] = exp2f((x[nt][e] - mb) * kLog2e);
+        l += p[nt][e];
+      }
+    if (__any_sync(0xffffffffu, av != 1.f)) {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[j][h][i4][r] *= av;
+    }
+    uint4 a;
+    split2(p[0][0] * wv, p[0][1] * wv, a.x, a.y);
+    split2(p[1][0] * wv, p[1][1] * wv, a.z, a.w);
+    if (is_page) {
+#pragma unroll
+      for (int j = 0; j < J; ++j)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint4 w = *reinterpret_cast<const uint4*>(sb + i8_off_vcodes(D) + j * 1024 + h * 512 + lane * 16);
+          mma16816(acc[j][h][0], a, i8_lo2(w.x), i8_hi2(w.x));
+          mma16816(acc[j][h][1], a, i8_lo2(w.y), i8_hi2(w.y));
+          mma16816(acc[j][h][2], a, i8_lo2(w.z), i8_hi2(w.z));
+          mma16816(acc[j][h][3], a, i8_lo2(w.w), i8_hi2(w.w));
+        }
+    } else {
+      const __half* ring = C.win_v + ((size_t)cb * P.hkv + g) * C.ring * D;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        uint32_t r[4][4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const int pos = pos0 + 4 * t4 + t;
+          uint4 w = make_uint4(0, 0, 0, 0);
+          if (pos < live_to) w = *reinterpret_cast<const uint4*>(ring + (size_t)(pos % C.ring) * D + 64 * j + 8 * g8);
+          r[t][0] = w.x, r[t][1] = w.y, r[t][2] = w.z, r[t][3] = w.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          mma16816(acc[j][e >> 2][e & 3], a, __byte_perm(r[0][e >> 1], r[1][e >> 1], e & 1 ? 0x7632 : 0x5410),
+                   __byte_perm(r[2][e >> 1], r[3][e >> 1], e & 1 ? 0x7632 : 0x5410));
+      }
+    }
+  }
+
+  // the warps meet: weights relative to the block's maximum, partial sums in true units
+  l += __shfl_xor_sync(0xffffffffu, l, 1);
+  l += __shfl_xor_sync(0xffffffffu, l, 2);
+  if (t4 == 0) {
+    sh.m[warp][g8] = m;
+    sh.l[warp][g8] = l;
+  }
+  const float unit = vref * (1.f / kWeightTop);
+  float* mine = merge + ((size_t)warp * 8 + g8) * D;
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int c = 0; c < 2; ++c)  // column 2 t4 + c: dims 64 j + 16 t4 + 8 c + 4 h + i
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<float4*>(mine + 64 * j + 16 * t4 + 8 * c + 4 * h) =
+            make_float4((acc[j][h][0][c] + acc[j][h][0][c + 2]) * unit, (acc[j][h][1][c] + acc[j][h][1][c + 2]) * unit,
+                        (acc[j][h][2][c] + acc[j][h][2][c + 2]) * unit, (acc[j][h][3][c] + acc[j][h][3][c + 2]) * unit);
+  __syncthreads();
+  for (int i = tid; i < G * D; i += kThreads) {
+    const int h = i / D, j = i % D;
+    float M = sh.m[0][h];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sh.m[w][h]);
+    const float mb = M == -INFINITY ? 0.f : M;
+    float sum = 0.f, o = 0.f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float f = exp2f((sh.m[w][h] - mb) * kLog2e);
+      sum = fmaf(f, sh.l[w][h], sum);
+      o = fmaf(f, merge[((size_t)w * 8 + h) * D + j], o);
+    }
+    if (S == 1) {
+      // nothing visible: 0 and -inf; a NaN sum passes through
+      if (j < P.dh) out[(head0 + h) * P.dh + j] = sum == 0.f ? 0.f : o / sum;
+      if (lse && j == 0) lse[head0 + h] = sum == 0.f ? -INFINITY : M + logf(sum);
+    } else {
+      reinterpret_cast<float*>(ws + L.acc)[((head0 + h) * S + s) * D + j] = o;
+      if (j == 0) {
+        float* ml = reinterpret_cast<float*>(ws + L.ml) + ((head0 + h) * S + s) * 2;
+        ml[0] = M;
+        ml[1] = sum;
+      }
+    }
+  }
+}
+
+// Joins the splits of one query head in their order.
+template <int D>
+__global__ void __launch_bounds__(D / 4) i8_combine_kernel(const unsigned char* ws, WsLayout L, int hq, int dh, float* out,
+                                                           float* lse) {
+  const int S = L.n_comp_splits, j = threadIdx.x;
+  const size_t head = (size_t)blockIdx.y * hq + blockIdx.x;
+  const float2* ml = reinterpret_cast<const float2*>(ws + L.ml) + head * S;
+  const float4* acc = reinterpret_cast<const float4*>(ws + L.acc) + head * S * (D / 4) + j;
+  float M = -INFINITY;
+  for (int s = 0; s < S; ++s) M = fmaxf(M, ml[s].x);
+  const float mb = M == -INFINITY ? 0.f : M;
+  float sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < S; ++s) {
+    const float f = exp2f((ml[s].x - mb) * kLog2e);
+    const float4 a = acc[(size_t)s * (D / 4)];
+    sum = fmaf(f, ml[s].y, sum);
+    o.x = fmaf(f, a.x, o.x);
+    o.y = fmaf(f, a.y, o.y);
+    o.z = fmaf(f, a.z, o.z);
+    o.w = fmaf(f, a.w, o.w);
+  }
+  const float z = sum == 0.f ? 0.f : 1.f / sum;
+  if (4 * j < dh) *reinterpret_cast<float4*>(out + head * dh + 4 * j) = make_float4(o.x * z, o.y * z, o.z * z, o.w * z);
+  if (lse && j == 0) lse[head] = sum == 0.f ? -INFINITY : M + logf(sum);
+}
+
+template <int D>
+cudaError_t decode(const KParams& P, const KCache& C, const void* q, int dtype, float scale, const int32_t* pages,
+                   const int32_t* counts, int n_sel, float* out, float* lse, float* scores, unsigned char* ws,
+                   const WsLayout& L, int max_ctx, cudaStream_t st) {
+  const size_t dyn = (size_t)kWarps * 8 * D * sizeof(float);
+  const dim3 grid(L.n_comp_splits, P.hkv, C.batch);
+  i8_decode_kernel<D><<<grid, kThreads, dyn, st>>>(P, C, q, dtype, scale, pages, counts, n_sel, out, lse, scores, ws, L,
+                                                   max_ctx);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || L.n_comp_splits == 1) return e;
+  i8_combine_kernel<D><<<dim3(P.hq, C.batch), D / 4, 0, st>>>(ws, L, P.hq, P.dh, out, lse);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// At most max_items groups of 16 tokens a sequence (pages and window), split so that the grid fills the
+// SMs twice over, but a split keeps two groups for each of its warps.
+WsLayout int8_ws_layout(const KParams& P, int batch, long long max_items, int n_splits, int num_sms) {
+  WsLayout L{};
+  long long S = n_splits;
+  if (S <= 0) {
+    const long long units = std::max(1LL, (long long)batch * P.hkv);
+    S = (2LL * ctas_per_sm(P.d) * num_sms + units - 1) / units;
+    S = std::min(S, (max_items + 2 * kWarps - 1) / (2 * kWarps));
+  }
+  S = std::max(1LL, std::min(S, std::min(max_items, 65535LL)));
+  L.n_comp_splits = (int)S;
+  const size_t heads = (size_t)batch * P.hq;
+  size_t o = 0;
+  if (S > 1) {
+    L.ml = o;
+    o = align256(o + heads * S * 2 * sizeof(float));
+    L.acc = o;
+    o = align256(o + heads * S * (size_t)P.d * sizeof(float));
+  }
+  L.total = std::max<size_t>(o, 256);
+  return L;
+}
+
+cudaError_t launch_int8_decode(const KParams& P, const KCache& C, const void* q, int dtype, float scale, const int32_t* pages,
+                               const int32_t* counts, int n_sel, float* out, float* lse, float* scores, void* ws,
+                               const WsLayout& L, int max_ctx, cudaStream_t st) {
+  unsigned char* w = reinterpret_cast<unsigned char*>(ws);
+  if (P.d == 128)
+    return decode<128>(P, C, q, dtype, scale, pages, counts, n_sel, out, lse, scores, w, L, max_ctx, st);
+  return decode<256>(P, C, q, dtype, scale, pages, counts, n_sel, out, lse, scores, w, L, max_ctx, st);
+}
+
+cudaError_t read_clear_int8_decode_error(unsigned* bits) {
+  unsigned zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(bits, g_int8_decode_err, sizeof(unsigned));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_int8_decode_err, &zero, sizeof(unsigned));
+}
+
+}  // namespace tq

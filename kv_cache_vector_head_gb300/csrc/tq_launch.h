@@ -46,6 +46,35 @@ cudaError_t launch_prefill_tiles(const KParams& P, const KCache& V, int n_query,
                                  float scale, float* out, float* lse, void* ws, const WsLayout& L, int max_ctx,
                                  cudaStream_t st);
 
+// 8-bit arm: whole sequences, direct page-aligned slots, one decode step (advances the counters), values read back.
+cudaError_t launch_int8_prefill_cache(const KParams& P, const KCache& C, const void* k, const void* v, int dtype, int n_tok,
+                                      int n_c, cudaStream_t st);
+cudaError_t launch_int8_direct(const KParams& P, const KCache& C, const void* k, const void* v, int dtype, long long n_tok,
+                               const long long* slots, cudaStream_t st);
+cudaError_t launch_int8_step(const KParams& P, const KCache& C, const void* k, const void* v, int dtype, cudaStream_t st);
+cudaError_t launch_int8_read(const KParams& P, const KCache& C, void* k, void* v, int dtype, int first, int n_tok,
+                             cudaStream_t st);
+
+// Decode of the 8-bit arm over at most max_items groups of 16 tokens a sequence; pages / counts: the page
+// ordinals of every (sequence, KV head), n_sel a row, or null for all pages.
+WsLayout int8_ws_layout(const KParams& P, int batch, long long max_items, int n_splits, int num_sms);
+cudaError_t launch_int8_decode(const KParams& P, const KCache& C, const void* q, int dtype, float scale, const int32_t* pages,
+                               const int32_t* counts, int n_sel, float* out, float* lse, float* scores, void* ws,
+                               const WsLayout& L, int max_ctx, cudaStream_t st);
+
+// Page selection, attention totals and eviction.
+size_t select_ws_bytes(const KParams& P, int batch, int max_ctx);
+cudaError_t launch_select(const KParams& P, const KCache& C, const void* q, int dtype, int k, int n_sink, int n_recent,
+                          int32_t* pages, int32_t* counts, void* ws, int max_ctx, cudaStream_t st);
+cudaError_t launch_track(const KParams& P, const KCache& C, const float* scores, const float* lse, float* mass, int max_ctx,
+                         cudaStream_t st);
+int evict_ring_limit();  // longest ring that is moved in place
+cudaError_t launch_evict(const KParams& P, const KCache& A, const KCache& B, const float* mass, float* mass_out, int budget,
+                         int n_sink, int n_recent, int32_t* kept, void* ws, cudaStream_t st);
+
+cudaError_t read_clear_int8_error(unsigned* bits);
+cudaError_t read_clear_int8_decode_error(unsigned* bits);
+cudaError_t read_clear_pages_error(unsigned* bits);
 cudaError_t read_clear_quant_error(unsigned* bits);
 cudaError_t read_clear_decode_error(unsigned* bits);
 #ifdef TQ_TEST_HOOKS

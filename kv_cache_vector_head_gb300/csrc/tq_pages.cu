@@ -1,0 +1,472 @@
+// Choosing pages: the pages a decode step reads (int8 arm) and the pages a cache keeps (every arm).
+//
+//   select   score(page) = float(max_g sum_j max(qi_gj kmax_j, qi_gj kmin_j)) * ks, qi = the group's queries on one
+//            int8 grid; the k best of a (sequence, KV head), the first n_sink and the last n_recent always among them
+//   track    mass[b][page] += sum over heads and the page's tokens of exp(l - lse)
+//   evict    the `budget` heaviest pages of a sequence stay, the first n_sink and the last n_recent always among them
+//
+// Both choices take the larger number first and the lower page among equals.  The scores are products of codes
+// summed in integers and then rounded once, the masses are compared as they are stored, so a choice never depends
+// on the order of a sum.
+#include <algorithm>
+
+#include "tq_int8.cuh"
+#include "tq_launch.h"
+
+namespace tq {
+
+static __device__ unsigned int g_pages_err = 0;
+
+namespace {
+
+constexpr int kPickThreads = 1024;
+constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kKeyCache = 40960;  // keys kept in shared memory (160 KB); longer lists are re-read from L2
+
+// Order-preserving map of a float to an unsigned integer (-0 counts as 0, NaN as the least).
+__device__ __forceinline__ uint32_t order_key(float x) {
+  if (x != x) return 0u;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+struct PickShared {
+  unsigned hist[256];
+  unsigned prefix, need;
+  int gt[kPickWarps], eq[kPickWarps];
+};
+
+// The `keep` of n items (keep < n) that stay: the first n_sink, the last n_recent, and of the rest
+// the largest keys, the lower index among equals.  Calls emit(i, stays, r) for every i < n, r = how many lower
+// items stay.  key(i) gives an item's order key.  All threads of the block.
+template <typename Key, typename Emit>
+__device__ void pick(PickShared& sh, uint32_t* cache, int n, int keep, int n_sink, int n_recent, Key key, Emit emit) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lo = min(n_sink, n), hi = max(lo, n - n_recent);  // the free items
+  int need = keep - lo - (n - hi);                             // how many of them stay (0 <= need < hi - lo)
+  need = max(0, need);
+  const bool cached = n <= kKeyCache;
+  if (cached)
+    for (int i = lo + tid; i < hi; i += kPickThreads) cache[i] = key(i);
+  auto get = [&](int i) -> uint32_t { return cached ? cache[i] : key(i); };
+  // the need-th largest key, 8 bits at a time
+  uint32_t prefix = 0, mask = 0;
+  unsigned left = (unsigned)need;
+  for (int shift = 24; shift >= 0 && need > 0; shift -= 8) {
+    if (tid < 256) sh.hist[tid] = 0;
+    __syncthreads();
+    for (int i = lo + tid; i < hi; i += kPickThreads) {
+      const uint32_t k = get(i);
+      if ((k & mask) == prefix) atomicAdd(&sh.hist[k >> shift & 255u], 1u);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      // lane i counts bins 255 - 8 i .. 248 - 8 i
+      unsigned c[8], sum = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += c[e] = sh.hist[255 - 8 * lane - e];
+      unsigned before = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const unsigned v = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += v;
+      }
+      before -= sum;
+      if (before < left && left <= before + sum) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (before < left && left <= before + c[e]) {
+            sh.prefix = prefix | (uint32_t)(255 - 8 * lane - e) << shift;
+            sh.need = left - before;
+          }
+          before += c[e];
+        }
+      }
+    }
+    __syncthreads();
+    prefix = sh.prefix;
+    left = sh.need;
+    mask |= 255u << shift;
+    __syncthreads();
+  }
+  // every warp takes a run of items: how many are above the threshold and how many on it
+  const int run = ((n + kPickWarps - 1) / kPickWarps + 31) & ~31;
+  const int a = min(n, warp * run), z = min(n, a + run);
+  auto kind = [&](int i) -> int {  // 2: stays, 1: stays while there is need, 0: goes
+    if (i < lo || i >= hi) return 2;
+    if (need == 0) return 0;
+    const uint32_t k = get(i);
+    return k > prefix ? 2 : k == prefix ? 1 : 0;
+  };
+  __syncthreads();  // (the key cache, where no pass ran)
+  int gt = 0, eq = 0;
+  for (int i0 = a; i0 < z; i0 += 32) {
+    const int t = i0 + lane < z ? kind(i0 + lane) : 0;
+    gt += __popc(__ballot_sync(0xffffffffu, t == 2));
+    eq += __popc(__ballot_sync(0xffffffffu, t == 1));
+  }
+  if (lane == 0) {
+    sh.gt[warp] = gt;
+    sh.eq[warp] = eq;
+  }
+  __syncthreads();
+  int rank = 0, ties = 0;  // of lower warps
+  for (int w = 0; w < warp; ++w) {
+    rank += sh.gt[w] + min(sh.eq[w], max(0, (int)left - ties));
+    ties += sh.eq[w];
+  }
+  const unsigned below = (1u << lane) - 1u;
+  for (int i0 = a; i0 < z; i0 += 32) {
+    const int i = i0 + lane;
+    const int t = i < z ? kind(i) : 0;
+    const unsigned ones = __ballot_sync(0xffffffffu, t == 1);
+    const bool stays = t == 2 || (t == 1 && ties + __popc(ones & below) < (int)left);
+    const unsigned in = __ballot_sync(0xffffffffu, stays);
+    if (i < z) emit(i, stays, rank + __popc(in & below));
+    rank += __popc(in);
+    ties += __popc(ones);
+  }
+}
+
+// ------------------------------------------------------------------ select
+
+constexpr int kScoreThreads = 256;
+constexpr int kScorePages = 4;  // pages a thread carries: a query word read from shared memory serves four products
+
+// order keys of the page scores, grid (page blocks, hkv, batch).  D / 16 lanes share a page, 16 channels each.
+template <int D>
+__global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_constant__ KParams P,
+                                                                   const __grid_constant__ KCache C, const void* q,
+                                                                   int dtype, int k, uint32_t* keys, int np_max, int max_ctx) {
+  constexpr int LP = D / 16;                   // lanes a page
+  constexpr int PB = kScoreThreads / LP * kScorePages;  // pages a block
+  __shared__ uint4 qpos[8][LP], qneg[8][LP];   // codes of the positive and of the negative queries
+  __shared__ float wmax[kScoreThreads / 32];
+  const int g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, G = P.G;
+  const int n = C.seq_len[b], nc = C.n_compressed[b];
+  if (n < 0 || n > max_ctx || nc < 0 || nc > n || nc / kPage > C.max_pages) {
+    if (tid == 0 && blockIdx.x == 0 && g == 0) atomicOr(&g_pages_err, TQ_DEVERR_SEQ_LEN);
+    return;
+  }
+  const int np = nc / kPage, p0 = blockIdx.x * PB;
+  if (np <= k || p0 >= np) return;  // every page is taken, or none is here
+  // one scale for the group's queries
+  const size_t row0 = (size_t)b * P.hq + (size_t)g * G;
+  float a = 0.f;
+  for (int i = tid; i < G * P.dh; i += kScoreThreads) a = fmaxf(a, i8_mag(load_elem(q, dtype, (long long)(row0 * P.dh + i))));
+  a = warp_max_f(a);
+  if (lane == 0) wmax[tid >> 5] = a;
+  __syncthreads();
+  a = wmax[0];
+#pragma unroll
+  for (int w = 1; w < kScoreThreads / 32; ++w) a = fmaxf(a, wmax[w]);
+  const float s = i8_scale(a), inv = s > 0.f ? __frcp_rn(s) : 0.f;
+  for (int i = tid; i < G * D; i += kScoreThreads) {
+    const int h = i / D, j = i % D;
+    const float x = j < P.dh ? load_elem(q, dtype, (long long)((row0 + h) * P.dh + j)) : 0.f;
+    const int c = (int)(i8_code(x, s, inv) & 255u) - 128;
+    reinterpret_cast<int8_t*>(&qpos[h][0])[j] = (int8_t)max(c, 0);
+    reinterpret_cast<int8_t*>(&qneg[h][0])[j] = (int8_t)min(c, 0);
+  }
+  __syncthreads();
+  const int l = tid % LP, slot = tid / LP;
+  uint4 lo[kScorePages], hi[kScorePages];
+  float ks[kScorePages];
+  int pg[kScorePages];
+#pragma unroll
+  for (int u = 0; u < kScorePages; ++u) {
+    pg[u] = p0 + u * (kScoreThreads / LP) + slot;
+    lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
+    ks[u] = 0.f;
+    if (pg[u] < np) {
+      const long long page = C.block_table[(size_t)b * C.max_pages + pg[u]];
+      if (page < 0 || page >= C.n_pages) {
+        if (l == 0) atomicOr(&g_pages_err, TQ_DEVERR_PAGE_INDEX);
+      } else {
+        const unsigned char* sb = i8_subblock(P, C, page, g);
+        lo[u] = *reinterpret_cast<const uint4*>(sb + 16 * l);
+        hi[u] = *reinterpret_cast<const uint4*>(sb + D + 16 * l);
+        ks[u] = *reinterpret_cast<const float*>(sb + i8_off_head(D));
+      }
+    }
+  }
+  int best[kScorePages];
+#pragma unroll
+  for (int u = 0; u < kScorePages; ++u) best[u] = INT32_MIN;
+  for (int h = 0; h < G; ++h) {
+    const uint4 qp = qpos[h][l], qn = qneg[h][l];
+#pragma unroll
+    for (int u = 0; u < kScorePages; ++u) {
+      int v = __dp4a((int)qp.x, (int)hi[u].x, 0);
+      v = __dp4a((int)qp.y, (int)hi[u].y, v);
+      v = __dp4a((int)qp.z, (int)hi[u].z, v);
+      v = __dp4a((int)qp.w, (int)hi[u].w, v);
+      v = __dp4a((int)qn.x, (int)lo[u].x, v);
+      v = __dp4a((int)qn.y, (int)lo[u].y, v);
+      v = __dp4a((int)qn.z, (int)lo[u].z, v);
+      v = __dp4a((int)qn.w, (int)lo[u].w, v);
+#pragma unroll
+      for (int o = 1; o < LP; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      best[u] = max(best[u], v);
+    }
+  }
+  if (l == 0) {
+    uint32_t* row = keys + ((size_t)b * P.hkv + g) * np_max;
+#pragma unroll
+    for (int u = 0; u < kScorePages; ++u)
+      if (pg[u] < np) row[pg[u]] = order_key(__fmul_rn((float)best[u], ks[u]));
+  }
+}
+
+// One block a (KV head, sequence): the list of its k pages, ascending, -1 behind.
+__global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const __grid_constant__ KCache C, int hkv,
+                                                                 const uint32_t* keys, int np_max, int k, int n_sink,
+                                                                 int n_recent, int32_t* pages, int32_t* counts, int max_ctx) {
+  extern __shared__ uint32_t cache[];
+  __shared__ PickShared sh;
+  const int g = blockIdx.x, b = blockIdx.y;
+  const size_t row = (size_t)b * hkv + g;
+  const int n = C.seq_len[b], nc = C.n_compressed[b];
+  int np = nc / kPage;
+  if (n < 0 || n > max_ctx || nc < 0 || nc > n || np > C.max_pages) np = 0;  // (flagged by the score kernel)
+  int32_t* list = pages + row * k;
+  const int taken = min(np, k);
+  if (threadIdx.x == 0) counts[row] = taken;
+  for (int i = taken + threadIdx.x; i < k; i += kPickThreads) list[i] = -1;
+  if (np <= k) {
+    for (int i = threadIdx.x; i < np; i += kPickThreads) list[i] = i;
+    return;
+  }
+  const uint32_t* kr = keys + row * np_max;
+  pick(sh, cache, np, k, n_sink, n_recent, [&](int i) { return kr[i]; },
+       [&](int i, bool stays, int r) {
+         if (stays) list[r] = i;
+       });
+}
+
+// ------------------------------------------------------------------ track
+
+constexpr int kTrackWarps = 8;
+
+// One block eight pages (128 tokens, four lanes of four tokens a page), its warps take the heads in turn.
+template <bool VEC>
+__global__ void __launch_bounds__(32 * kTrackWarps) track_kernel(const __grid_constant__ KCache C, int hq,
+                                                                 const float* __restrict__ scores,
+                                                                 const float* __restrict__ lse, float* mass, int max_ctx) {
+  __shared__ float part[kTrackWarps][8];
+  const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = C.seq_len[b];
+  int nc = C.n_compressed[b];
+  if (n < 0 || n > max_ctx || nc < 0 || nc > n || (nc + kPage - 1) / kPage > C.max_pages) {
+    if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(&g_pages_err, TQ_DEVERR_SEQ_LEN);
+    return;
+  }
+  const int t0 = blockIdx.x * 128;
+  if (t0 >= nc) return;
+  const int tok = t0 + 4 * lane;
+  float sum = 0.f;
+#pragma unroll 4
+  for (int h = warp; h < hq; h += kTrackWarps) {
+    const size_t row = (size_t)b * hq + h;
+    const float z = lse[row];
+    const float* p = scores + row * max_ctx + tok;
+    float x[4];
+    if (VEC && tok + 3 < nc) {
+      const float4 v = *reinterpret_cast<const float4*>(p);
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = tok + e < nc ? p[e] : -INFINITY;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum += tok + e < nc ? expf(x[e] - z) : 0.f;
+  }
+  sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+  sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+  if ((lane & 3) == 0) part[warp][lane >> 2] = sum;
+  __syncthreads();
+  if (threadIdx.x < 8) {
+    const int page = t0 / kPage + threadIdx.x;
+    if (page * kPage < nc) {
+      float s = part[0][threadIdx.x];
+#pragma unroll
+      for (int w = 1; w < kTrackWarps; ++w) s += part[w][threadIdx.x];
+      mass[(size_t)b * C.max_pages + page] += s;
+    }
+  }
+}
+
+// ------------------------------------------------------------------ evict
+
+// Pages dropped from a sequence, -1 where its counters are no valid state.
+__device__ __forceinline__ int dropped(const KCache& C, int b, int budget) {
+  const int n = C.seq_len[b], nc = C.n_compressed[b];
+  if (nc < 0 || n < nc || (nc + kPage - 1) / kPage > C.max_pages) return -1;
+  return max(0, nc / kPage - budget);
+}
+
+// Window rows move with their positions: p becomes p - 16 e, so ring slot i takes slot (i + 16 e) mod ring.
+// grid (column slices, 2 hkv, batch); in place through shared memory, else straight across.
+__global__ void __launch_bounds__(256) evict_window_kernel(const __grid_constant__ KCache A, const __grid_constant__ KCache B,
+                                                           int hkv, int d, int budget, int cols) {
+  extern __shared__ uint4 buf[];  // [ring][cols / 8]
+  const int b = blockIdx.z, head = blockIdx.y >> 1, ring = A.ring;
+  const bool is_key = (blockIdx.y & 1) == 0;
+  const size_t base = ((size_t)b * hkv + head) * ring * d;
+  const __half* src = (is_key ? A.win_k : A.win_v) + base;
+  __half* dst = (is_key ? B.win_k : B.win_v) + base;
+  const int e = max(0, dropped(A, b, budget));
+  const int by = (int)((long long)e * kPage % ring);
+  const int c0 = blockIdx.x * cols, cu = min(cols, d - c0) / 8, total = ring * cu;
+  const bool here = src == dst;
+  if (here && by == 0) return;
+  for (int i = threadIdx.x; i < total; i += blockDim.x) {
+    const int r = i / cu, c = i % cu;
+    int from = r + by;
+    if (from >= ring) from -= ring;
+    const uint4 w = *reinterpret_cast<const uint4*>(src + (size_t)from * d + c0 + 8 * c);
+    if (here) buf[i] = w;
+    else *reinterpret_cast<uint4*>(dst + (size_t)r * d + c0 + 8 * c) = w;
+  }
+  if (!here) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < total; i += blockDim.x)
+    *reinterpret_cast<uint4*>(dst + (size_t)(i / cu) * d + c0 + 8 * (i % cu)) = buf[i];
+}
+
+// One block a sequence: block table (kept pages in order, a partly filled page, the dropped pages, the rest), masses,
+// counters.  New rows are put together in the workspace first, as the outputs may be the inputs.
+__global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_constant__ KCache A,
+                                                                  const __grid_constant__ KCache B, const float* mass,
+                                                                  float* mass_out, int budget, int n_sink, int n_recent,
+                                                                  int32_t* kept, int32_t* ws) {
+  extern __shared__ uint32_t cache[];
+  __shared__ PickShared sh;
+  const int b = blockIdx.x, mp = A.max_pages;
+  const int n = A.seq_len[b], nc = A.n_compressed[b], e = dropped(A, b, budget);
+  const int32_t* table = A.block_table + (size_t)b * mp;
+  int32_t* table_out = const_cast<int32_t*>(B.block_table) + (size_t)b * mp;
+  const float* m = mass + (size_t)b * mp;
+  float* m_out = mass_out + (size_t)b * mp;
+  int32_t* list = kept ? kept + (size_t)b * budget : nullptr;
+  if (e < 0 && threadIdx.x == 0) atomicOr(&g_pages_err, TQ_DEVERR_SEQ_LEN);
+  const int np = e < 0 ? 0 : nc / kPage, keep = np - max(e, 0);
+  if (list)
+    for (int i = keep + threadIdx.x; i < budget; i += kPickThreads) list[i] = -1;
+  if (e <= 0) {  // nothing goes: the state as it is
+    const int held = e < 0 ? mp : (nc + kPage - 1) / kPage;
+    for (int i = threadIdx.x; i < mp; i += kPickThreads) {
+      const int32_t page = table[i];
+      const float x = m[i];
+      table_out[i] = page;
+      m_out[i] = i < held ? x : 0.f;
+      if (list && i < keep) list[i] = i;
+    }
+    if (threadIdx.x == 0) {
+      B.seq_len[b] = n;
+      B.n_compressed[b] = nc;
+    }
+    return;
+  }
+  int32_t* wt = ws + (size_t)b * 2 * mp;
+  float* wm = reinterpret_cast<float*>(wt + mp);
+  const int part = nc % kPage ? 1 : 0;  // a partly filled page stays behind the kept ones
+  pick(sh, cache, np, keep, n_sink, n_recent, [&](int i) { return order_key(m[i]); },
+       [&](int i, bool stays, int r) {
+         if (stays) {
+           wt[r] = table[i];
+           wm[r] = m[i];
+           if (list) list[r] = i;
+         } else {
+           wt[keep + part + i - r] = table[i];
+         }
+       });
+  if (part && threadIdx.x == 0) {
+    wt[keep] = table[np];
+    wm[keep] = m[np];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < mp; i += kPickThreads) {
+    const int32_t page = i < np + part ? wt[i] : table[i];
+    const float x = i < keep + part ? wm[i] : 0.f;
+    table_out[i] = page;
+    m_out[i] = x;
+  }
+  if (threadIdx.x == 0) {
+    B.seq_len[b] = n - kPage * e;
+    B.n_compressed[b] = nc - kPage * e;
+  }
+}
+
+size_t key_cache_bytes(int n) { return (size_t)std::min(n, kKeyCache) * sizeof(uint32_t); }
+
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes) {
+  if (bytes <= 40 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
+}  // namespace
+
+size_t select_ws_bytes(const KParams& P, int batch, int max_ctx) {
+  const size_t np = std::max(1, max_ctx / kPage);
+  return std::max<size_t>(256, (size_t)batch * P.hkv * np * sizeof(uint32_t));
+}
+
+cudaError_t launch_select(const KParams& P, const KCache& C, const void* q, int dtype, int k, int n_sink, int n_recent,
+                          int32_t* pages, int32_t* counts, void* ws, int max_ctx, cudaStream_t st) {
+  const int np = std::max(1, max_ctx / kPage);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(ws);
+  const int pb = kScoreThreads / (P.d / 16) * kScorePages;
+  const dim3 grid((np + pb - 1) / pb, P.hkv, C.batch);
+  if (P.d == 128) page_score_kernel<128><<<grid, kScoreThreads, 0, st>>>(P, C, q, dtype, k, keys, np, max_ctx);
+  else page_score_kernel<256><<<grid, kScoreThreads, 0, st>>>(P, C, q, dtype, k, keys, np, max_ctx);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const size_t dyn = key_cache_bytes(np);
+  if ((e = allow_smem(page_pick_kernel, dyn)) != cudaSuccess) return e;
+  page_pick_kernel<<<dim3(P.hkv, C.batch), kPickThreads, dyn, st>>>(C, P.hkv, keys, np, k, n_sink, n_recent, pages, counts,
+                                                                   max_ctx);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_track(const KParams& P, const KCache& C, const float* scores, const float* lse, float* mass, int max_ctx,
+                         cudaStream_t st) {
+  const dim3 grid((max_ctx + 127) / 128, C.batch);
+  // rows of scores start on 16 bytes where max_ctx is a multiple of 4 and the array does
+  if (max_ctx % 4 == 0 && (reinterpret_cast<uintptr_t>(scores) & 15) == 0)
+    track_kernel<true><<<grid, 32 * kTrackWarps, 0, st>>>(C, P.hq, scores, lse, mass, max_ctx);
+  else
+    track_kernel<false><<<grid, 32 * kTrackWarps, 0, st>>>(C, P.hq, scores, lse, mass, max_ctx);
+  return cudaGetLastError();
+}
+
+int evict_ring_limit() { return 200 * 1024 / 16; }
+
+cudaError_t launch_evict(const KParams& P, const KCache& A, const KCache& B, const float* mass, float* mass_out, int budget,
+                         int n_sink, int n_recent, int32_t* kept, void* ws, cudaStream_t st) {
+  cudaError_t e;
+  if (A.ring > 0) {
+    // whole rows where the ring's rows fit 48 KB, else the widest slice of columns that does, at least 8
+    int cols = P.d;
+    while (cols > 8 && (size_t)A.ring * cols * 2 > 48 * 1024) cols /= 2;
+    const size_t dyn = A.win_k == B.win_k ? (size_t)A.ring * cols * 2 : 0;
+    if ((e = allow_smem(evict_window_kernel, dyn)) != cudaSuccess) return e;
+    evict_window_kernel<<<dim3((P.d + cols - 1) / cols, 2 * P.hkv, A.batch), 256, dyn, st>>>(A, B, P.hkv, P.d, budget, cols);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  const size_t dyn = key_cache_bytes(A.max_pages);
+  if ((e = allow_smem(evict_pick_kernel, dyn)) != cudaSuccess) return e;
+  evict_pick_kernel<<<A.batch, kPickThreads, dyn, st>>>(A, B, mass, mass_out, budget, n_sink, n_recent, kept,
+                                                       reinterpret_cast<int32_t*>(ws));
+  return cudaGetLastError();
+}
+
+cudaError_t read_clear_pages_error(unsigned* bits) {
+  unsigned zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(bits, g_pages_err, sizeof(unsigned));
+  if (e != cudaSuccess) return e;
+  return cudaMemcpyToSymbol(g_pages_err, &zero, sizeof(unsigned));
+}
+
+}  // namespace tq

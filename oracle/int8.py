@@ -1,0 +1,96 @@
+"""The 8-bit arm in float64: page codes, the page's bytes, attention over the cache, page selection and eviction.
+
+A page holds 16 tokens of one KV head.  scale = max |x| / 127 over the page (one float32 quotient, 0 below
+float32's normal range), code = nearest integer to x / scale with ties to even; the keys' smallest and largest code
+of a channel bound what any query can score against the page.
+"""
+
+from __future__ import annotations
+
+import numpy as np
+
+PAGE = 16
+
+
+def quantize_page(x):
+    """x [16, d] float64 holding the stored inputs exactly -> (codes int [16, d], scale float32)."""
+    x = np.asarray(x, dtype=np.float64)
+    fin = np.isfinite(x)
+    amax = np.float32(np.max(np.abs(np.where(fin, x, 0.0)), initial=0.0))
+    s = np.float32(amax / np.float32(127))
+    if s < np.finfo(np.float32).tiny:
+        return np.zeros(x.shape, np.int64), np.float32(0)
+    with np.errstate(invalid="ignore"):
+        c = np.rint(x / np.float64(s))  # a quotient of floats is a half step or off it by 2^-32 at least: exact here
+    c = np.where(np.isnan(x), 0, np.clip(c, -127, 127))
+    return c.astype(np.int64), s
+
+
+def pack_page(k, v):
+    """The sub-block bytes of a page from keys and values [16, d]."""
+    d = k.shape[1]
+    (kc, ks), (vc, vs) = quantize_page(k), quantize_page(v)
+    head = np.zeros(8, np.float32)
+    head[0], head[1] = ks, vs
+    out = [kc.min(0).astype(np.int8).tobytes(), kc.max(0).astype(np.int8).tobytes(), head.tobytes()]
+    keys = np.zeros((2, d // 64, 8, 4, 16), np.uint8)
+    vals = np.zeros((d // 64, 2, 8, 4, 4, 4), np.uint8)
+    for t in range(PAGE):
+        for c in range(d):
+            g, n = 2 * (t // 4) + t % 2, t % 4 // 2
+            keys[n, c // 64, g, c % 64 // 16, c % 16] = kc[t, c] + 128
+            vals[c // 64, c % 8 // 4, c % 64 // 8, t // 4, c % 4, t % 4] = vc[t, c] + 128
+    return np.frombuffer(b"".join(out) + keys.tobytes() + vals.tobytes(), np.uint8)
+
+
+def dequantize(x):
+    """x [n, d], n a multiple of 16 -> the values that its pages stand for, float64."""
+    x = np.asarray(x, np.float64)
+    y = np.empty_like(x)
+    for i in range(0, len(x), PAGE):
+        c, s = quantize_page(x[i:i + PAGE])
+        y[i:i + PAGE] = c * np.float64(s)
+    return y
+
+
+def n_compressed(T, window):
+    return PAGE * (max(0, T - window) // PAGE)
+
+
+def held(x, nc):
+    """The values a cache holds for one head's inputs x [T, d]: pages up to nc, float16 behind."""
+    x = np.asarray(x, np.float64)
+    with np.errstate(over="ignore"):
+        return np.concatenate([dequantize(x[:nc]), x[nc:].astype(np.float16).astype(np.float64)])
+
+
+def attend(q, k, v, scale):
+    """One head: q [d] over k, v [n, d] -> (out [d], lse, logits [n])."""
+    if len(k) == 0:
+        return np.zeros(v.shape[1]), -np.inf, np.zeros(0)
+    l = scale * (np.asarray(k, np.float64) @ np.asarray(q, np.float64))
+    m = l.max()
+    p = np.exp(l - m)
+    return p @ np.asarray(v, np.float64) / p.sum(), m + np.log(p.sum()), l
+
+
+def choose(key, keep, n_sink, n_recent):
+    """Indices that stay, ascending: forced ends, then the larger key, the lower index among equals."""
+    n = len(key)
+    if n <= keep:
+        return list(range(n))
+    forced = set(range(min(n, n_sink))) | set(range(max(0, n - n_recent), n))
+    # a NaN counts least
+    rest = sorted((i for i in range(n) if i not in forced), key=lambda i: (-np.inf if np.isnan(key[i]) else key[i], -i), reverse=True)
+    return sorted(list(forced) + rest[: keep - len(forced)])
+
+
+def page_scores(q, k, nc):
+    """q [G, d], k [T, d] inputs of one head -> float32 score of every full page."""
+    qc, _ = quantize_page(np.asarray(q, np.float64))
+    out = []
+    for i in range(0, nc, PAGE):
+        c, s = quantize_page(k[i:i + PAGE])
+        top = np.maximum(qc * c.min(0), qc * c.max(0)).sum(1).max()
+        out.append(np.float32(top) * s)
+    return np.array(out, np.float32)
