@@ -22,7 +22,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUDA_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "-Xptxas", "-O3"]
 SOURCES = ["tq_host.cpp", "tq_api.cu", "tq_quantize.cu", "tq_decode.cu",
-           "tq_int8_cache.cu", "tq_int8_decode.cu", "tq_pages.cu"]
+           "tq_int8_cache.cu", "tq_int8_decode.cu", "tq_int8_prefill.cu", "tq_pages.cu"]
 
 
 def nvcc() -> str:

@@ -221,6 +221,10 @@ static WsLayout decode_layout(const KParams& K, int batch, int max_ctx, int n_sp
 // Prefill workspace: the virtual sequences' counters and parent rows, then a decode workspace
 // for batch * n_query sequences.
 static size_t prefill_layout(const KParams& K, int batch, int n_query, int max_ctx, WsLayout* L) {
+  if (K.int8 && int8_prefill_tc_ok(K, n_query)) {
+    *L = int8_prefill_layout(K, batch, n_query, max_ctx, num_sms());
+    return L->total;
+  }
   const size_t head = ((size_t)3 * batch * n_query * sizeof(int32_t) + 255) & ~(size_t)255;
   const int S = !K.int8 && prefill_tiles_ok(K) ? prefill_tile_splits(K, batch, n_query, max_ctx, num_sms()) : 0;
   *L = decode_layout(K, batch * n_query, max_ctx, S);
@@ -396,6 +400,12 @@ extern "C" tq_status tq_prefill_attention(const tq_layer_params* p, const tq_cac
     return TQ_ERR_CAPACITY;
   }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+  if (K.int8 && int8_prefill_tc_ok(K, n_query)) {
+    if ((long long)cache->batch * L.n_comp_splits > 65535)
+      return fail(TQ_ERR_INVALID_ARG, "batch times splits must be <= 65535");
+    return cuda_status(launch_int8_prefill(K, C, n_query, q, dtype, scale, out, lse, workspace, L, max_ctx, st),
+                       "tq_prefill_attention");
+  }
   const size_t nv = (size_t)cache->batch * n_query;
   int32_t* seq_v = reinterpret_cast<int32_t*>(workspace);
   int32_t* nc_v = seq_v + nv;
@@ -421,13 +431,14 @@ extern "C" tq_status tq_prefill_attention(const tq_layer_params* p, const tq_cac
 extern "C" tq_status tq_check_device_error(tq_stream_t stream, uint32_t* bits_out) {
   cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_status(e, "tq_check_device_error: stream");
-  unsigned a = 0, b = 0, c = 0, d = 0, f = 0;
+  unsigned a = 0, b = 0, c = 0, d = 0, f = 0, g = 0;
   if ((e = read_clear_quant_error(&a)) != cudaSuccess) return cuda_status(e, "tq_check_device_error");
   if ((e = read_clear_decode_error(&b)) != cudaSuccess) return cuda_status(e, "tq_check_device_error");
   if ((e = read_clear_int8_error(&c)) != cudaSuccess) return cuda_status(e, "tq_check_device_error");
   if ((e = read_clear_int8_decode_error(&d)) != cudaSuccess) return cuda_status(e, "tq_check_device_error");
   if ((e = read_clear_pages_error(&f)) != cudaSuccess) return cuda_status(e, "tq_check_device_error");
-  a |= b | c | d | f;
+  if ((e = read_clear_int8_prefill_error(&g)) != cudaSuccess) return cuda_status(e, "tq_check_device_error");
+  a |= b | c | d | f | g;
   if (bits_out) *bits_out = a;
   if (a) {
     set_error("device error word 0x%x", a);

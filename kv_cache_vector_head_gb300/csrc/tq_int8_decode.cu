@@ -385,8 +385,7 @@ cudaError_t decode(const KParams& P, const KCache& C, const void* q, int dtype, 
                                                    max_ctx);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || L.n_comp_splits == 1) return e;
-  i8_combine_kernel<D><<<dim3(P.hq, C.batch), D / 4, 0, st>>>(ws, L, P.hq, P.dh, out, lse);
-  return cudaGetLastError();
+  return launch_int8_combine(P, ws, L, C.batch, out, lse, st);
 }
 
 }  // namespace
@@ -422,6 +421,14 @@ cudaError_t launch_int8_decode(const KParams& P, const KCache& C, const void* q,
   if (P.d == 128)
     return decode<128>(P, C, q, dtype, scale, pages, counts, n_sel, out, lse, scores, w, L, max_ctx, st);
   return decode<256>(P, C, q, dtype, scale, pages, counts, n_sel, out, lse, scores, w, L, max_ctx, st);
+}
+
+cudaError_t launch_int8_combine(const KParams& P, const unsigned char* ws, const WsLayout& L, long long rows, float* out,
+                                float* lse, cudaStream_t st) {
+  const dim3 grid(P.hq, (unsigned)rows);
+  if (P.d == 128) i8_combine_kernel<128><<<grid, 32, 0, st>>>(ws, L, P.hq, P.dh, out, lse);
+  else i8_combine_kernel<256><<<grid, 64, 0, st>>>(ws, L, P.hq, P.dh, out, lse);
+  return cudaGetLastError();
 }
 
 cudaError_t read_clear_int8_decode_error(unsigned* bits) {

@@ -62,6 +62,16 @@ cudaError_t launch_int8_decode(const KParams& P, const KCache& C, const void* q,
                                const int32_t* counts, int n_sel, float* out, float* lse, float* scores, void* ws,
                                const WsLayout& L, int max_ctx, cudaStream_t st);
 
+// Joins the splits of rows x hq query rows (L.ml, L.acc) in their order.
+cudaError_t launch_int8_combine(const KParams& P, const unsigned char* ws, const WsLayout& L, long long rows, float* out,
+                                float* lse, cudaStream_t st);
+
+// Prefill attention of the 8-bit arm on tcgen05 (d = 128, more than 16 rows a KV head).
+bool int8_prefill_tc_ok(const KParams& P, int n_query);
+WsLayout int8_prefill_layout(const KParams& P, int batch, int n_query, int max_ctx, int num_sms);
+cudaError_t launch_int8_prefill(const KParams& P, const KCache& C, int n_query, const void* q, int dtype, float scale,
+                                float* out, float* lse, void* ws, const WsLayout& L, int max_ctx, cudaStream_t st);
+
 // Page selection, attention totals and eviction.
 size_t select_ws_bytes(const KParams& P, int batch, int max_ctx);
 cudaError_t launch_select(const KParams& P, const KCache& C, const void* q, int dtype, int k, int n_sink, int n_recent,
@@ -74,6 +84,7 @@ cudaError_t launch_evict(const KParams& P, const KCache& A, const KCache& B, con
 
 cudaError_t read_clear_int8_error(unsigned* bits);
 cudaError_t read_clear_int8_decode_error(unsigned* bits);
+cudaError_t read_clear_int8_prefill_error(unsigned* bits);
 cudaError_t read_clear_pages_error(unsigned* bits);
 cudaError_t read_clear_quant_error(unsigned* bits);
 cudaError_t read_clear_decode_error(unsigned* bits);
