@@ -347,8 +347,8 @@ __global__ void __launch_bounds__(kThreads) i8_decode_kernel(const __grid_consta
   }
 }
 
-// Joins the splits of one query head in their order.
-template <int D>
+// Joins the splits of one query head in their order; LOG2: their references are powers of two, else of e.
+template <int D, bool LOG2>
 __global__ void __launch_bounds__(D / 4) i8_combine_kernel(const unsigned char* ws, WsLayout L, int hq, int dh, float* out,
                                                            float* lse) {
   const int S = L.n_comp_splits, j = threadIdx.x;
@@ -362,7 +362,8 @@ __global__ void __launch_bounds__(D / 4) i8_combine_kernel(const unsigned char* 
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int s = 0; s < S; ++s) {
-    const float f = exp2f((ml[s].x - mb) * kLog2e);
+    const float f = exp2f((ml[s].x - mb) * (LOG2 ? 1.f : kLog2e));
+    if (ml[s].y == 0.f) continue;  // a split that saw nothing may not have written its sums
     const float4 a = acc[(size_t)s * (D / 4)];
     sum = fmaf(f, ml[s].y, sum);
     o.x = fmaf(f, a.x, o.x);
@@ -372,7 +373,7 @@ __global__ void __launch_bounds__(D / 4) i8_combine_kernel(const unsigned char* 
   }
   const float z = sum == 0.f ? 0.f : 1.f / sum;
   if (4 * j < dh) *reinterpret_cast<float4*>(out + head * dh + 4 * j) = make_float4(o.x * z, o.y * z, o.z * z, o.w * z);
-  if (lse && j == 0) lse[head] = sum == 0.f ? -INFINITY : M + logf(sum);
+  if (lse && j == 0) lse[head] = sum == 0.f ? -INFINITY : (LOG2 ? M * 0.6931471805599453f : M) + logf(sum);
 }
 
 template <int D>
@@ -385,7 +386,7 @@ cudaError_t decode(const KParams& P, const KCache& C, const void* q, int dtype, 
                                                    max_ctx);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || L.n_comp_splits == 1) return e;
-  return launch_int8_combine(P, ws, L, C.batch, out, lse, st);
+  return launch_int8_combine(P, ws, L, C.batch, false, out, lse, st);
 }
 
 }  // namespace
@@ -423,11 +424,11 @@ cudaError_t launch_int8_decode(const KParams& P, const KCache& C, const void* q,
   return decode<256>(P, C, q, dtype, scale, pages, counts, n_sel, out, lse, scores, w, L, max_ctx, st);
 }
 
-cudaError_t launch_int8_combine(const KParams& P, const unsigned char* ws, const WsLayout& L, long long rows, float* out,
-                                float* lse, cudaStream_t st) {
+cudaError_t launch_int8_combine(const KParams& P, const unsigned char* ws, const WsLayout& L, long long rows, bool log2,
+                                float* out, float* lse, cudaStream_t st) {
   const dim3 grid(P.hq, (unsigned)rows);
-  if (P.d == 128) i8_combine_kernel<128><<<grid, 32, 0, st>>>(ws, L, P.hq, P.dh, out, lse);
-  else i8_combine_kernel<256><<<grid, 64, 0, st>>>(ws, L, P.hq, P.dh, out, lse);
+  auto kern = P.d == 128 ? (log2 ? i8_combine_kernel<128, true> : i8_combine_kernel<128, false>) : i8_combine_kernel<256, false>;
+  kern<<<grid, P.d / 4, 0, st>>>(ws, L, P.hq, P.dh, out, lse);
   return cudaGetLastError();
 }
 

@@ -7,15 +7,18 @@
 // by a power of two a row) or two limbs (float), and the weights P vs are two limbs, since one f16 limb would
 // leave 2^-12 of the float output: a tile costs one product for S (two for float queries) and two for O.
 //
-//   warps 0-3, 4-7   a unit each: one thread a row takes its S row from tensor memory (tcgen05.ld), keeps the
-//                    running maximum and sum, and writes P's limbs over S; then adds the tile's O to its 128
-//                    registers.  O starts anew in every tile: the tensor cores' accumulation truncates, which over a
-//                    long context would cost 2^-25 of the output a step, float additions round.
-//   warps 8-11       turn the tile's codes (and the float16 window rows) into f16 operands in shared memory, two
-//                    tiles ahead.
-//   warp 12          one thread issues tcgen05.mma; S_u of the next tile runs while the other unit is in its softmax.
+//   warps 0-7, 8-15  a unit each, two threads a row: each takes its half of the S row from tensor memory
+//                    (tcgen05.ld), the halves agree on the reference of the exponents, and write P's limbs over S.
+//                    The reference follows the running maximum only when that has grown by 2^8, so O stays as it is in
+//                    almost every tile.  O is added to memory (scratch, in L2) and begun anew every four
+//                    tiles: the tensor cores' accumulation truncates, 2^-25 of O a step; over the whole of a long
+//                    context that would be 1e-5, over four tiles it is under 1e-6.  (O in registers instead, added
+//                    after every tile, needs 130 a thread, 96 are there: its spills went to L2 and the chunk of
+//                    2048 queries over 16384 tokens took 1283 us.)
+//   warps 16-19      turn the tile's codes (and the float16 window rows) into f16 operands in shared memory.
+//   warp 20          one thread issues tcgen05.mma; S_u of the next tile runs while the other unit is in its softmax.
 // With one row tile (RT = 1: up to 128 rows, or float queries, whose second limb takes the second tile's
-// shared memory) the units take the key tiles in turn and join at the end.
+// shared memory) the units take the key tiles in turn, as two splits that the joining kernel adds up.
 #include <math.h>
 
 #include <algorithm>
@@ -30,11 +33,15 @@ static __device__ unsigned int g_int8_prefill_err = 0;
 namespace {
 
 constexpr int D = 128;
+constexpr int H = D / 2;             // columns of S and channels of O that a softmax thread takes
 constexpr int KT = 128;              // tokens of a key tile
 constexpr int GROUPS = KT / kPage;
-constexpr int kThreads = 512;
+constexpr int kSoftWarps = 16, kConvWarps = 4;
+constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 1);
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kWeightTop = 16384.f;
+constexpr float kWeightTop = 64.f;   // weights reach 2^8 above it: 2^14 in f16
+constexpr float kSlack = 8.f;          // log2 of how far a score may pass the reference
+constexpr int kRun = 8;                // tiles that O gathers in tensor memory
 
 // Shared-memory operands without swizzle: core matrices of 8 rows x 16 bytes; LBO steps along the contraction
 // (8 elements), SBO along the rows (8).
@@ -42,21 +49,23 @@ constexpr uint32_t kQLbo = 128, kQSbo = 2048, kQTile = 128 * D * 2;
 constexpr uint32_t kKLbo = 144, kKSbo = 16 * 144;               // keys: rows tokens
 constexpr uint32_t kVSbo = 144, kVLbo = 16 * 144 + 64;          // values: rows channels, contraction tokens
 constexpr uint32_t kKTile = 16 * kKSbo, kVTile = 16 * kVLbo;
-constexpr int kStages = 2;
-constexpr uint32_t kSmemQ = 0, kSmemK = 2 * kQTile, kSmemV = kSmemK + kStages * kKTile;
-constexpr uint32_t kSmemBytes = kSmemV + kStages * kVTile;
+constexpr uint32_t kRawK = kI8Head + 16 * D, kRawV = 16 * D;    // a page's scales and keys, and its values, as in the pool
+constexpr uint32_t kRaw = kRawK + kRawV;
+constexpr uint32_t kSmemQ = 0, kSmemK = 2 * kQTile, kSmemV = kSmemK + 2 * kKTile, kSmemRaw = kSmemV + kVTile;
+constexpr uint32_t kSmemBytes = kSmemRaw + GROUPS * kRaw;
 constexpr int kIdesc = (1 << 4) | ((128 >> 3) << 17) | ((128 >> 4) << 24);  // f16 x f16 -> f32, M = N = 128
 
 struct Shared {
-  uint64_t kfull[kStages], vfull[kStages], kfree[kStages], vfree[kStages];
+  uint64_t kfull[2], kfree[2], vfull, vfree, info[4];
   uint64_t sfull[2], pready[2], ofull[2], drained;
-  float2 scale[kStages][GROUPS];  // key and value scale of a group of 16 tokens
-  uint32_t live[kStages];         // groups whose page is there
-  uint32_t bad[kStages][GROUPS];  // window tokens with non-finite values
+  uint64_t rawk[GROUPS], rawv[GROUPS];
+  float2 scale[4][GROUPS];  // tile modulo 4: key and value scale of a group of 16 tokens
+  uint32_t live[4];         // groups whose page is there; 8 bits on, groups with bad tokens
+  uint32_t bad[4][GROUPS];  // window tokens with non-finite values
   float rowscale[256];            // 1 / the power of two of a query row
-  float m[128], l[128];
+  float mx[2][2][2][128];         // tile parity, unit, half: largest score of a row's half
+  float l[2][2][128];
   uint32_t tmem;
-  int fail;
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
@@ -98,22 +107,22 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
       "r"(a), "l"(b), "r"(kIdesc), "r"(accum)
       : "memory");
 }
-__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&v)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-      : "r"(a));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
 __device__ __forceinline__ void tmem_ld16(uint32_t a, uint32_t (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
         "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(a));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_ld16x2(uint32_t a, uint32_t (&v)[16], uint32_t (&w)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+      "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(w[0]),
+        "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]), "=r"(w[8]), "=r"(w[9]),
+        "=r"(w[10]), "=r"(w[11]), "=r"(w[12]), "=r"(w[13]), "=r"(w[14]), "=r"(w[15])
       : "r"(a));
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
@@ -135,6 +144,112 @@ __device__ __forceinline__ uint32_t pack_f16(float a, float b) {
 }
 __device__ __forceinline__ float pow2_above(float s) { return __uint_as_float((__float_as_uint(s) + 0x007fffffu) & 0x7f800000u); }
 __device__ __forceinline__ float pow2_inv(float v) { return __uint_as_float(0x7f000000u - __float_as_uint(v)); }
+
+__device__ __forceinline__ uint64_t pair2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair2(uint64_t p, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(p)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+// f16 pair of (a, b) and of what it leaves (exact differences: one mixed fused multiply-add each)
+__device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t& lo) {
+  float x, y;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(b), "f"(a));
+  asm("{\n .reg .f16 p, q, n;\n mov.b32 {p, q}, %2;\n mov.b16 n, 0xBC00;\n"
+      " fma.rn.f32.f16 %0, p, n, %3;\n fma.rn.f32.f16 %1, q, n, %4;\n}\n"
+      : "=f"(x), "=f"(y)
+      : "r"(hi), "f"(a), "f"(b));
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(y), "f"(x));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Largest score (powers of two) of a row's 64 columns at ts; sc: the four groups' scales.  FULL: all are visible and there;
+// else columns 0 .. see of the groups in `live`.
+template <bool FULL>
+__device__ __forceinline__ float largest(uint32_t ts, const float2* sc, float fq, int see, uint32_t live) {
+  float mx = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    uint32_t v[2][16];
+    tmem_ld16x2(ts + 32 * c, v[0], v[1]);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int gi = 2 * c + h, lim = (live >> gi & 1) ? see - 16 * gi : -1;
+      float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        float x[4] = {__uint_as_float(v[h][i]), __uint_as_float(v[h][i + 1]), __uint_as_float(v[h][8 + i]), __uint_as_float(v[h][9 + i])};
+        if (!FULL) {
+          x[0] = i <= lim ? x[0] : -INFINITY;
+          x[1] = i + 1 <= lim ? x[1] : -INFINITY;
+          x[2] = 8 + i <= lim ? x[2] : -INFINITY;
+          x[3] = 9 + i <= lim ? x[3] : -INFINITY;
+        }
+        a0 = max3(a0, x[0], x[1]);
+        a1 = max3(a1, x[2], x[3]);
+      }
+      // (-inf times a scale of 0 is NaN, which fmaxf leaves out)
+      mx = fmaxf(mx, fmaxf(a0, a1) * (sc[gi].x * fq));
+    }
+  }
+  return mx;
+}
+
+// The weights of a row's 64 columns relative to 2^mb, times the value scale and vi, as f16 limbs over the scores (of each
+// 16 columns: hi limbs in 0 .. 7, lo limbs in 8 .. 15); returns the sum of the weights proper.
+template <bool FULL>
+__device__ __forceinline__ float weights(uint32_t ts, const float2* scales, float fq, float mb, float vi, int see, uint32_t live) {
+  const uint64_t nmb = pair2(-mb, -mb);
+  uint64_t ls = 0;
+#pragma unroll
+  for (int gi = 0; gi < 4; ++gi) {
+    const float2 sc = scales[gi];
+    const uint64_t f = pair2(sc.x * fq, sc.x * fq), wv = pair2(sc.y * vi, sc.y * vi);
+    const int lim = (live >> gi & 1) ? see - 16 * gi : -1;  // tokens 0 .. lim of the group
+    uint32_t v[16], pk[16];
+    tmem_ld16(ts + 16 * gi, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float e0, e1;
+      unpair2(fma2(pair2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f, nmb), e0, e1);
+      e0 = ex2(e0);
+      e1 = ex2(e1);
+      if (!FULL) {
+        e0 = 2 * i <= lim ? e0 : 0.f;
+        e1 = 2 * i + 1 <= lim ? e1 : 0.f;
+      }
+      uint64_t e = pair2(e0, e1);
+      ls = add2(ls, e);
+      e = mul2(e, wv);
+      unpair2(e, e0, e1);
+      split2(e0, e1, pk[i], pk[8 + i]);
+    }
+    tmem_st16(ts + 16 * gi, pk);
+  }
+  float l0, l1;
+  unpair2(ls, l0, l1);
+  return l0 + l1;
+}
 
 // RT row tiles of 128, QL query limbs (RT + QL = 3).  grid (row tiles, hkv, batch * splits).
 template <int RT, int QL>
@@ -174,43 +289,52 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
   if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(&sh.kfull[i], 4);
-      mbar_init(&sh.vfull[i], 4);
-      mbar_init(&sh.kfree[i], 1);
-      mbar_init(&sh.vfree[i], 1);
+    mbar_init(&sh.vfull, kConvWarps);
+    mbar_init(&sh.vfree, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.info[i], kConvWarps);
+    for (int i = 0; i < GROUPS; ++i) {
+      mbar_init(&sh.rawk[i], 1);
+      mbar_init(&sh.rawv[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.kfull[i], kConvWarps);
+      mbar_init(&sh.kfree[i], 1);
       mbar_init(&sh.sfull[i], 1);
-      mbar_init(&sh.pready[i], 128);
+      mbar_init(&sh.pready[i], 8);
       mbar_init(&sh.ofull[i], 1);
     }
     mbar_init(&sh.drained, 1);
-    sh.fail = 0;
+    for (int i = 0; i < 4; ++i) sh.live[i] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   // ---- queries: a warp a row; the sign of the scale goes into them, so that larger stays larger
   const float sgn = scale < 0.f ? -1.f : 1.f;
-  for (int r = warp; r < 128 * RT; r += kThreads / 32) {
-    float x[4] = {0.f, 0.f, 0.f, 0.f};
-    const int rr = row0 + r;
-    if (rr < rows && 4 * lane < P.dh) {
-      const long long at = (((long long)b * n_query + rr / G) * P.hq + (long long)g * G + rr % G) * P.dh + 4 * lane;
+  for (int rb = 4 * warp; rb < 128 * RT; rb += 4 * kThreads / 32) {
+    float x[4][4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = load_elem(q, dtype, at + e) * sgn;
+    for (int e = 0; e < 4; ++e) {  // four rows' loads in flight
+      const int rr = row0 + rb + e;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[e][i] = 0.f;
+      if (rr < rows && 4 * lane < P.dh) {
+        const long long at = (((long long)b * n_query + rr / G) * P.hq + (long long)g * G + rr % G) * P.dh + 4 * lane;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[e][i] = load_elem(q, dtype, at + i);
+      }
     }
-    const float a = warp_max_f(fmaxf(fmaxf(i8_mag(x[0]), i8_mag(x[1])), fmaxf(i8_mag(x[2]), i8_mag(x[3]))));
-    const int e2 = a > 0.f ? min(max(140 - (int)(__float_as_uint(a) >> 23), -113), 126) : 0;
-    const float up = __uint_as_float((uint32_t)(127 + e2) << 23);
-    if (lane == 0) sh.rowscale[r] = __uint_as_float((uint32_t)(127 - e2) << 23);
-    const uint32_t at = (uint32_t)(r >> 7) * kQTile + (uint32_t)((r & 127) >> 3) * kQSbo + (r & 7) * 16 + (lane >> 1) * kQLbo + (lane & 1) * 8;
-    const __half2 h0 = __floats2half2_rn(x[0] * up, x[1] * up), h1 = __floats2half2_rn(x[2] * up, x[3] * up);
-    *reinterpret_cast<uint2*>(smem + kSmemQ + at) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&h0), *reinterpret_cast<const uint32_t*>(&h1));
-    if (QL == 2) {
-      const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-      *reinterpret_cast<uint2*>(smem + kSmemQ + kQTile + at) =
-          make_uint2(pack_f16(x[0] * up - f0.x, x[1] * up - f0.y), pack_f16(x[2] * up - f1.x, x[3] * up - f1.y));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int r = rb + e;
+      const float a = warp_max_f(fmaxf(fmaxf(i8_mag(x[e][0]), i8_mag(x[e][1])), fmaxf(i8_mag(x[e][2]), i8_mag(x[e][3]))));
+      const int e2 = a > 0.f ? min(max(140 - (int)(__float_as_uint(a) >> 23), -113), 126) : 0;
+      const float up = __uint_as_float((uint32_t)(127 + e2) << 23) * sgn;
+      if (lane == 0) sh.rowscale[r] = __uint_as_float((uint32_t)(127 - e2) << 23);
+      const uint32_t at = (uint32_t)(r >> 7) * kQTile + (uint32_t)((r & 127) >> 3) * kQSbo + (r & 7) * 16 + (lane >> 1) * kQLbo + (lane & 1) * 8;
+      uint32_t hi[2], lo[2];
+      split2(x[e][0] * up, x[e][1] * up, hi[0], lo[0]);
+      split2(x[e][2] * up, x[e][3] * up, hi[1], lo[1]);
+      *reinterpret_cast<uint2*>(smem + kSmemQ + at) = make_uint2(hi[0], hi[1]);
+      if (QL == 2) *reinterpret_cast<uint2*>(smem + kSmemQ + kQTile + at) = make_uint2(lo[0], lo[1]);
     }
   }
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -219,258 +343,313 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_after();
   const uint32_t tmem = sh.tmem;  // units' S / P at 0 and 128, their O at 256 and 384
 
-  if (warp < 8) {
-    // ------------------------------------------------------------ softmax of unit u
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
-    const int u = warp >> 2, r = tid & 127;
+  if (warp < kSoftWarps) {
+    // ------------------------------------------------------------ softmax: unit u, columns and channels 64 hf ..
+    const int u = warp >> 3, hf = (warp >> 2) & 1, r = tid & 127;
     const int rr = row0 + (RT == 2 ? u * 128 : 0) + r;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t ts = tmem + lanes + 128u * u, to = tmem + lanes + 256u + 128u * u;
+    const uint32_t ts = tmem + lanes + 128u * u + 64u * hf, to = ts + 256u;
     const int pos = rr < rows ? (int)max(-1LL, row_pos(rr)) : -1;
     const float fq = sh.rowscale[(RT == 2 ? u * 128 : 0) + r] * fabsf(scale) * kLog2e;
-    float o[D];
-#pragma unroll
-    for (int i = 0; i < D; ++i) o[i] = 0.f;
-    float m = -INFINITY, l = 0.f, vref = 0.f;
-    uint32_t ph = 0;
+    const size_t head = ((size_t)b * n_query + rr / G) * P.hq + (size_t)g * G + rr % G;
+    const bool direct = RT == 2 && S == 1;
+    const int sx = RT == 2 ? split : 2 * split + u, SX = RT == 2 ? S : 2 * S;
+    // where the row's sums gather: four channels of 128 rows side by side, so that a warp's accesses are contiguous
+    const size_t block = ((size_t)blockIdx.z * gridDim.y + g) * gridDim.x + blockIdx.x;
+    float4* gather = reinterpret_cast<float4*>(ws + L.afrag) + ((block * 2 + u) * 2 + hf) * (H / 4 * 128) + r;
+    float m = -INFINITY, l = 0.f, vref = 0.f;  // reference of the exponents, sum, reference of the value scales
+    float since = 1.f;                         // what the gathered sums have to be scaled by
+    bool have = false;                         // something has been gathered
+    int idx = 0;                               // tiles of this unit so far
     bool failed = false;
-    for (int j = j0 + (RT == 1 ? u : 0); j < j1; j += RT == 1 ? 2 : 1, ph ^= 1) {
-      const int st = (j - j0) & 1, sp = ((j - j0) >> 1) & 1;
-      if (!mbar_wait(&sh.vfull[st], sp) || !mbar_wait(&sh.sfull[u], ph)) {
-        failed = true;
-        break;
+    // gathered = gathered * since + O
+    auto gather_o = [&]() {
+      const bool scaled = __any_sync(0xffffffffu, since != 1.f);
+#pragma unroll 1
+      for (int c = 0; c < H / 16; ++c) {
+        uint32_t v[16];
+        tmem_ld16(to + 16 * c, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float4* at = gather + (4 * c + i) * 128;
+          float4 x = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
+                                 __uint_as_float(v[4 * i + 3]));
+          if (have && !scaled) {
+            // (one thread owns the place: the additions' order is the tiles' order)
+            asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(at), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w) : "memory");
+            continue;
+          }
+          if (have) {
+            const float4 a = __ldcg(at);
+            x = make_float4(fmaf(a.x, since, x.x), fmaf(a.y, since, x.y), fmaf(a.z, since, x.z), fmaf(a.w, since, x.w));
+          }
+          __stcg(at, x);
+        }
       }
+      have = true;
+      since = 1.f;
+    };
+    for (int j = j0 + (RT == 1 ? u : 0); j < j1; j += RT == 1 ? 2 : 1, ++idx) {
+      const int st = (j - j0) & 3;
+      // (after a wait ran out a thread waits no more, but keeps to the barriers it shares with others)
+      failed = failed || !mbar_wait(&sh.info[st], ((j - j0) >> 2) & 1) || !mbar_wait(&sh.sfull[u], idx & 1);
       tc_after();
-      const uint32_t live = sh.live[st];
-      const int see = pos - j * KT;  // columns 0 .. see are visible
-      float mx = -INFINITY, vn = vref;
+      const uint32_t there = sh.live[st], live = (there >> (4 * hf)) & 15u;
+      const int see = pos - j * KT - 64 * hf;  // columns 0 .. see of the half are visible
+      const bool full = __all_sync(0xffffffffu, see >= 63) && live == 15u;
+      // the tile's largest value scale
+      const float vt = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(pow2_above(sh.scale[st][lane & 7].y))));
+      float mx = full ? largest<true>(ts, sh.scale[st] + 4 * hf, fq, see, live) : largest<false>(ts, sh.scale[st] + 4 * hf, fq, see, live);
+      float* box = &sh.mx[idx & 1][u][0][0];
+      box[128 * hf + r] = mx;
+      asm volatile("bar.sync %0, 256;" ::"r"(1 + u) : "memory");
+      mx = fmaxf(mx, box[128 * (hf ^ 1) + r]);
+      // both halves of a row come to the same reference
+      float factor = 1.f;
+      if (mx > m + kSlack) {
+        factor = ex2(m - mx);  // 0 from the first score on
+        m = mx;
+        l *= factor;
+      }
+      if (vt > vref) {
+        factor *= vref * pow2_inv(vt);
+        vref = vt;
+      }
+      const bool begin = idx % kRun == 0;
+      if (begin ? idx > 0 : __any_sync(0xffffffffu, factor != 1.f)) {
+        failed = failed || !mbar_wait(&sh.ofull[u], (idx - 1) & 1);
+        tc_after();
+        if (begin) {
+          gather_o();
+        } else {
+#pragma unroll 1
+          for (int c = 0; c < H / 16; ++c) {
+            uint32_t v[16];
+            tmem_ld16(to + 16 * c, v);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t v[32];
-        tmem_ld32(ts + 32 * c, v);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int gi = 2 * c + h;
-          float a = -INFINITY;
-          if (see >= 16 * gi + 15) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) a = fmaxf(a, __uint_as_float(v[16 * h + i]));
-          } else {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (16 * gi + i <= see) a = fmaxf(a, __uint_as_float(v[16 * h + i]));
+            for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) * factor);
+            tmem_st16(to + 16 * c, v);
           }
-          const float2 sc = sh.scale[st][gi];
-          if (live >> gi & 1) mx = fmaxf(mx, a == -INFINITY ? a : a * (sc.x * fq));
-          vn = fmaxf(vn, pow2_above(sc.y));
         }
       }
-      const float mn = fmaxf(m, mx), mb = mn == -INFINITY ? 0.f : mn;
-      const float al = ex2(m - mb);
-      const float av = vn > 0.f ? al * (vref * pow2_inv(vn)) : al;
-      const float vi = vn > 0.f ? pow2_inv(vn) : 0.f;
-      m = mn;
-      vref = vn;
-      l *= al;
-#pragma unroll
-      for (int gi = 0; gi < GROUPS; ++gi) {
-        uint32_t v[16], pk[16];
-        tmem_ld16(ts + 16 * gi, v);
-        const float2 sc = sh.scale[st][gi];
-        const float f = sc.x * fq, wv = sc.y * vi * kWeightTop;
-        const int lim = (live >> gi & 1) ? see - 16 * gi : -1;  // tokens 0 .. lim of the group
-        float ls = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float e0 = ex2(fmaf(__uint_as_float(v[2 * i]), f, -mb)), e1 = ex2(fmaf(__uint_as_float(v[2 * i + 1]), f, -mb));
-          if (lim < 15) {
-            e0 = 2 * i <= lim ? e0 : 0.f;
-            e1 = 2 * i + 1 <= lim ? e1 : 0.f;
-          }
-          ls += e0 + e1;
-          e0 *= wv;
-          e1 *= wv;
-          const __half2 hh = __floats2half2_rn(e0, e1);
-          const float2 ff = __half22float2(hh);
-          pk[i] = *reinterpret_cast<const uint32_t*>(&hh);
-          pk[8 + i] = pack_f16(e0 - ff.x, e1 - ff.y);
+      since *= factor;
+      const float mb = m == -INFINITY ? 0.f : m, vi = vref > 0.f ? pow2_inv(vref) * kWeightTop : 0.f;
+      l += full ? weights<true>(ts, sh.scale[st] + 4 * hf, fq, mb, vi, see, live)
+                : weights<false>(ts, sh.scale[st] + 4 * hf, fq, mb, vi, see, live);
+      // infinities and NaN among the window's values lie as zeros in the tile, since zero weights of rows
+      // that do not see them would not cancel them: the rows that do see them take them here
+      if (there >> GROUPS) {
+        if (!have) {
+          for (int i = 0; i < H / 4; ++i) __stcg(gather + 128 * i, make_float4(0.f, 0.f, 0.f, 0.f));
+          have = true;
         }
-        l += ls;
-        tmem_st16(ts + 16 * gi, pk);  // hi limbs in columns 0 .. 7 of the group's 16, lo limbs in 8 .. 15
-      }
-      // window tokens with infinities or NaN among their values lie as zeros in the tile, since zero weights
-      // of rows that do not see them would not cancel them: the rows that do see them add them here
-      float keep = av;
-      uint32_t any = 0;
-#pragma unroll
-      for (int i = 0; i < GROUPS; ++i) any |= sh.bad[st][i];
-      if (any) {
-#pragma unroll
-        for (int i = 0; i < D; ++i) o[i] *= av;
-        keep = 1.f;
 #pragma unroll 1
         for (int t = 0; t < KT; ++t) {
           const int p = j * KT + t;
           if (!(sh.bad[st][t >> 4] >> (t & 15) & 1) || p > pos) continue;
-          const size_t at = (((size_t)b * P.hkv + g) * C.ring + p % C.ring) * D;
-          const long long qa = (((long long)b * n_query + rr / G) * P.hq + (long long)g * G + rr % G) * P.dh;
-          float dot = 0.f;
+          const __half* row = C.win_v + (((size_t)b * P.hkv + g) * C.ring + p % C.ring) * D + H * hf;
 #pragma unroll 1
-          for (int i = 0; i < P.dh; ++i) dot = fmaf(load_elem(q, dtype, qa + i), __half2float(C.win_k[at + i]), dot);
-          const float w = ex2(dot * (scale * kLog2e) - mb) * vi * kWeightTop;
-#pragma unroll
-          for (int i = 0; i < D; ++i) o[i] = fmaf(w, __half2float(C.win_v[at + i]), o[i]);
+          for (int i = 0; i < H; ++i) {
+            const float x = __half2float(row[i]);
+            float* at = reinterpret_cast<float*>(gather + (i >> 2) * 128) + (i & 3);
+            if (!(fabsf(x) <= 65504.f)) __stcg(at, __ldcg(at) + x);
+          }
         }
       }
       asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
       tc_before();
-      mbar_arrive(&sh.pready[u]);  // (nothing of the tile's scales is read after this)
-      if (!mbar_wait(&sh.ofull[u], ph)) {
-        failed = true;
-        break;
-      }
-      tc_after();
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        uint32_t v[16];
-        tmem_ld16(to + 16 * c, v);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) o[16 * c + i] = fmaf(o[16 * c + i], keep, __uint_as_float(v[i]));
-      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.pready[u]);  // (nothing of the tile's scales is read after this)
     }
+    if (idx > 0 && !failed && !mbar_wait(&sh.ofull[u], (idx - 1) & 1)) failed = true;
     if (failed) {
       atomicOr(&g_int8_prefill_err, TQ_DEVERR_TIMEOUT);
-      sh.fail = 1;
     }
-    const float unit = vref * (1.f / kWeightTop);
+    tc_after();
+    sh.l[u][hf][r] = l;
+    asm volatile("bar.sync %0, 256;" ::"r"(1 + u) : "memory");
+    l = sh.l[u][0][r] + sh.l[u][1][r];
+    // what is gathered and the last O, in true units, to the output row or to the split's partial sums
+    const float unit = vref * (1.f / kWeightTop), z = direct ? (l == 0.f ? 0.f : unit / l) : unit;
+    float* dst = direct ? out + head * P.dh + H * hf : reinterpret_cast<float*>(ws + L.acc) + (head * SX + sx) * D + H * hf;
+    const int width = rr >= rows ? 0 : direct ? min(H, P.dh - H * hf) : H;  // (a multiple of 4; can be negative)
+#pragma unroll 1
+    for (int c = 0; c < H / 16; ++c) {
+      uint32_t v[16];
+      if (idx > 0) {
+        tmem_ld16(to + 16 * c, v);
+      } else {
 #pragma unroll
-    for (int i = 0; i < D; ++i) o[i] *= unit;
-    if (RT == 1) {
-      // the units meet: unit 1 leaves its rows in the (now idle) operand memory, column by column
-      float* box = reinterpret_cast<float*>(smem + kSmemK);
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (u == 1) {
-#pragma unroll
-        for (int i = 0; i < D; ++i) box[i * 128 + r] = o[i];
-        sh.m[r] = m;
-        sh.l[r] = l;
+        for (int i = 0; i < 16; ++i) v[i] = 0;
       }
-      asm volatile("bar.sync 1, 256;" ::: "memory");
-      if (u == 0) {
-        const float m1 = sh.m[r], mn = fmaxf(m, m1), mb = mn == -INFINITY ? 0.f : mn;
-        const float f0 = ex2(m - mb), f1 = ex2(m1 - mb);
-        l = l * f0 + sh.l[r] * f1;
-        m = mn;
 #pragma unroll
-        for (int i = 0; i < D; ++i) o[i] = o[i] * f0 + box[i * 128 + r] * f1;
+      for (int i = 0; i < 4; ++i) {
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (have) a = __ldcg(gather + (4 * c + i) * 128);
+        a = make_float4(fmaf(a.x, since, __uint_as_float(v[4 * i])) * z, fmaf(a.y, since, __uint_as_float(v[4 * i + 1])) * z,
+                        fmaf(a.z, since, __uint_as_float(v[4 * i + 2])) * z, fmaf(a.w, since, __uint_as_float(v[4 * i + 3])) * z);
+        if (16 * c + 4 * i < width) *reinterpret_cast<float4*>(dst + 16 * c + 4 * i) = a;
       }
     }
-    if ((RT == 2 || u == 0) && rr < rows) {
-      const size_t head = ((size_t)b * n_query + rr / G) * P.hq + (size_t)g * G + rr % G;
-      if (S == 1) {
-        const float z = l == 0.f ? 0.f : 1.f / l;
-        float* dst = out + head * P.dh;
-#pragma unroll
-        for (int i = 0; i < D; i += 4)
-          if (i < P.dh) *reinterpret_cast<float4*>(dst + i) = make_float4(o[i] * z, o[i + 1] * z, o[i + 2] * z, o[i + 3] * z);
+    if (hf == 0 && rr < rows) {
+      if (direct) {
         if (lse) lse[head] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
       } else {
-        float* dst = reinterpret_cast<float*>(ws + L.acc) + (head * S + split) * D;
-#pragma unroll
-        for (int i = 0; i < D; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-        float* ml = reinterpret_cast<float*>(ws + L.ml) + (head * S + split) * 2;
-        ml[0] = m * 0.6931471805599453f;  // the joining kernel takes natural logarithms
+        float* ml = reinterpret_cast<float*>(ws + L.ml) + (head * SX + sx) * 2;
+        ml[0] = l == 0.f ? -INFINITY : m;  // in powers of two
         ml[1] = l;
       }
     }
-  } else if (warp < 12) {
+  } else if (warp < kSoftWarps + kConvWarps) {
     // ------------------------------------------------------------ operands: groups cw and cw + 4 of every tile
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
-    const int cw = warp - 8, g8 = lane >> 2, t4 = lane & 3;
-    uint4 kr[2][4], vr[2][4];
-    const unsigned char* sb[2];
-    float2 sc[2];
-    // page of group x (0, 1) of tile j: its sub-block, or null
-    auto page_of = [&](int j, int x) -> const unsigned char* {
-      const int p0 = j * KT + (cw + 4 * x) * kPage;
-      if (j >= j1 || p0 >= min(nc, end)) return nullptr;
-      const long long page = C.block_table[(size_t)b * C.max_pages + p0 / kPage];
-      if (page < 0 || page >= C.n_pages) {
-        if (lane == 0) atomicOr(&g_int8_prefill_err, TQ_DEVERR_PAGE_INDEX);
-        return nullptr;
-      }
-      return i8_subblock(P, C, page, g);
+    // Keys are stored two tiles ahead, values one tile after the products that read the last ones; each
+    // group's codes come as they lie in the pool, by bulk copies issued when the place has been read.
+    const int cw = warp - kSoftWarps, g8 = lane >> 2, t4 = lane & 3;
+    const int pages = min(nc, end + kPage - 1) / kPage;  // of the sequence that any row sees
+    const __half* wk = C.win_k + ((size_t)b * P.hkv + g) * C.ring * D;
+    const __half* wv = C.win_v + ((size_t)b * P.hkv + g) * C.ring * D;
+    auto read_id = [&](int j, int x) -> int {  // table entry of group x (0, 1) of tile j
+      const int pg = j * GROUPS + cw + 4 * x;
+      return j < j1 && pg < pages ? C.block_table[(size_t)b * C.max_pages + pg] : INT32_MIN;
     };
-    auto load_keys = [&](int j) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        sb[x] = page_of(j, x);
-        if (sb[x]) {
-          sc[x] = *reinterpret_cast<const float2*>(sb[x] + i8_off_head(D));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) kr[x][i] = *reinterpret_cast<const uint4*>(sb[x] + i8_off_kcodes(D) + i * 512 + lane * 16);
-        }
-      }
+    auto checked = [&](int id) -> int {  // -1 where there is no page
+      if (id >= 0 && id < C.n_pages) return id;
+      if (id != INT32_MIN && lane == 0) atomicOr(&g_int8_prefill_err, TQ_DEVERR_PAGE_INDEX);
+      return -1;
     };
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, mbar_wait(bar, parity)); };
+    auto fetch = [&](int id, int gi, bool values) {  // one lane
+      const uint32_t bar = smem_u32(values ? &sh.rawv[gi] : &sh.rawk[gi]), bytes = values ? kRawV : kRawK;
+      const uint32_t to = sbase + kSmemRaw + gi * kRaw + (values ? kRawK : 0);
+      const unsigned char* from = i8_subblock(P, C, id, g) + i8_off_head(D) + (values ? kRawK : 0);
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+      asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from),
+                   "r"(bytes), "r"(bar)
+                   : "memory");
+    };
+    // bits x (keys) and 2 + x (values): the parity of the group's next copy, and whether one is in flight
+    uint32_t phase = 0, fly = 0;
     bool failed = false;
-    load_keys(j0);
-    for (int j = j0; j < j1; ++j) {
+    // pages of the tile whose values come next (iv), of the one after it (in), of the one whose keys come next (ik),
+    // and the entry of the one after that as read
+    int iv[2], in[2], ik[2], far[2];
+    auto store_keys = [&](int j) {  // tile j's keys into their stage; the next copies of this warp's keys
       const int st = (j - j0) & 1, sp = ((j - j0) >> 1) & 1;
-      unsigned char* kt = smem + kSmemK + st * kKTile;
-      unsigned char* vt = smem + kSmemV + st * kVTile;
-      const unsigned char* cur[2] = {sb[0], sb[1]};
-      const float2 csc[2] = {sc[0], sc[1]};
-      if (!mbar_wait(&sh.kfree[st], sp ^ 1)) {
-        failed = true;
-        break;
-      }
+      if (!wait(&sh.kfree[st], sp ^ 1)) failed = true;
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int gi = cw + 4 * x, p0 = j * KT + gi * kPage;
+        const int gi = cw + 4 * x, p0 = (j * GROUPS + gi) * kPage;
+        unsigned char* kt = smem + kSmemK + st * kKTile + (2 * gi + (g8 >> 2)) * kKSbo + ((g8 >> 1 & 1) * 4 + (g8 & 1)) * 16 + 2 * t4 * kKLbo;
+        float2 sc = make_float2(1.f, p0 >= nc && p0 < end ? 1.f : 0.f);
+        uint32_t bad = 0;
+        if (ik[x] >= 0) {
+          if (!wait(&sh.rawk[gi], phase >> x & 1)) failed = true;
+          phase ^= 1u << x;
+          fly &= ~(1u << x);
+          const unsigned char* from = smem + kSmemRaw + gi * kRaw;
+          sc = *reinterpret_cast<const float2*>(from);
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          const int tok = 4 * (g8 >> 1) + 2 * nt + (g8 & 1), row = 16 * gi + tok;
-          unsigned char* dst = kt + (row >> 3) * kKSbo + (row & 7) * 16 + 2 * t4 * kKLbo;
-#pragma unroll
-          for (int jj = 0; jj < 2; ++jj) {
+          for (int i = 0; i < 4; ++i) {  // i = 2 nt + jj: token 4 (g8 / 2) + 2 nt + g8 % 2, channels 64 jj + 16 t4 ..
+            unsigned char* dst = kt + (i >> 1) * 32 + (i & 1) * 8 * kKLbo;
+            const uint4 w = *reinterpret_cast<const uint4*>(from + kI8Head + i * 512 + lane * 16);
+            *reinterpret_cast<uint4*>(dst) = make_uint4(i8_lo2(w.x), i8_hi2(w.x), i8_lo2(w.y), i8_hi2(w.y));
+            *reinterpret_cast<uint4*>(dst + kKLbo) = make_uint4(i8_lo2(w.z), i8_hi2(w.z), i8_lo2(w.w), i8_hi2(w.w));
+          }
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < 4; ++i) {
+            const int pos = p0 + 4 * (g8 >> 1) + 2 * (i >> 1) + (g8 & 1);
+            unsigned char* dst = kt + (i >> 1) * 32 + (i & 1) * 8 * kKLbo;
             uint4 a = make_uint4(0, 0, 0, 0), c = a;
-            if (cur[x]) {
-              const uint4 w = kr[x][2 * nt + jj];
-              a = make_uint4(i8_lo2(w.x), i8_hi2(w.x), i8_lo2(w.y), i8_hi2(w.y));
-              c = make_uint4(i8_lo2(w.z), i8_hi2(w.z), i8_lo2(w.w), i8_hi2(w.w));
-            } else if (p0 >= nc && p0 + tok < end) {
-              const __half* rowp = C.win_k + (((size_t)b * P.hkv + g) * C.ring + (p0 + tok) % C.ring) * D + 64 * jj + 16 * t4;
+            if (p0 >= nc && pos < end) {
+              const __half* rowp = wk + (size_t)(pos % C.ring) * D + 64 * (i & 1) + 16 * t4;
               a = *reinterpret_cast<const uint4*>(rowp);
               c = *reinterpret_cast<const uint4*>(rowp + 8);
             }
-            *reinterpret_cast<uint4*>(dst + 8 * jj * kKLbo) = a;
-            *reinterpret_cast<uint4*>(dst + (8 * jj + 1) * kKLbo) = c;
+            *reinterpret_cast<uint4*>(dst) = a;
+            *reinterpret_cast<uint4*>(dst + kKLbo) = c;
+          }
+          if (p0 >= nc) {
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+              const int pos = p0 + 4 * t4 + (i & 3);
+              if (pos >= end) continue;
+              const uint4 a = *reinterpret_cast<const uint4*>(wv + (size_t)(pos % C.ring) * D + 64 * (i >> 2) + 8 * g8);
+              const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                if ((w[e] & 0x7c00u) == 0x7c00u || (w[e] & 0x7c000000u) == 0x7c000000u) bad |= 1u << (4 * t4 + (i & 3));
+            }
+            bad = __reduce_or_sync(0xffffffffu, bad);
           }
         }
-        if (cur[x]) {  // the group's keys are on their way: its values take their registers
-#pragma unroll
-          for (int i = 0; i < 4; ++i) vr[x][i] = *reinterpret_cast<const uint4*>(cur[x] + i8_off_vcodes(D) + i * 512 + lane * 16);
+        // what the softmax takes of the tile; the place's readers of four tiles ago are done (the values of the tile
+        // before last were stored after the products of the one before it)
+        if (lane == 0) {
+          const int at = (j - j0) & 3;
+          sh.scale[at][gi] = sc;
+          sh.bad[at][gi] = bad;
+          const uint32_t bits = (uint32_t)(ik[x] >= 0 || (p0 >= nc && p0 < end)) | (bad ? 1u << GROUPS : 0u);
+          atomicAnd(&sh.live[at], ~((1u | 1u << GROUPS) << gi));
+          atomicOr(&sh.live[at], bits << gi);
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.kfull[st]);
-      load_keys(j + 1);
-      if (!mbar_wait(&sh.vfree[st], sp ^ 1)) {
+      if (lane == 0) {
+        mbar_arrive(&sh.kfull[st]);
+        mbar_arrive(&sh.info[(j - j0) & 3]);
+      }
+    };
+    auto next_keys = [&](int x, int id) {  // copies of the next tile's keys and values follow into places that were read
+      ik[x] = id;
+      if (id >= 0) {
+        if (lane == 0) fetch(id, cw + 4 * x, false);
+        fly |= 1u << x;
+      }
+    };
+    auto next_values = [&](int x, int id) {
+      iv[x] = id;
+      if (id >= 0) {
+        if (lane == 0) fetch(id, cw + 4 * x, true);
+        fly |= 4u << x;
+      }
+    };
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int id0 = checked(read_id(j0, x));
+      in[x] = checked(read_id(j0 + 1, x));
+      far[x] = read_id(j0 + 2, x);
+      next_keys(x, id0);
+      next_values(x, id0);
+    }
+    if (j0 < j1) store_keys(j0);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) next_keys(x, in[x]);
+    if (j0 + 1 < j1) store_keys(j0 + 1);
+    for (int j = j0; j < j1 && !failed; ++j) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        next_keys(x, checked(far[x]));  // tile j + 2
+        far[x] = read_id(j + 3, x);
+      }
+      if (!wait(&sh.vfree, ((j - j0) & 1) ^ 1)) {
         failed = true;
         break;
       }
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const int gi = cw + 4 * x, p0 = j * KT + gi * kPage;
-        const bool win = !cur[x] && p0 >= nc && p0 < end;
-        unsigned char* dst = vt + (2 * gi + (t4 >> 1)) * kVLbo + g8 * kVSbo + (t4 & 1) * 8;
-        uint32_t bad = 0;
-        if (!win) {
+        const int gi = cw + 4 * x, p0 = (j * GROUPS + gi) * kPage;
+        unsigned char* dst = smem + kSmemV + (2 * gi + (t4 >> 1)) * kVLbo + g8 * kVSbo + (t4 & 1) * 8;
+        if (iv[x] >= 0) {
+          if (!wait(&sh.rawv[gi], phase >> (2 + x) & 1)) failed = true;
+          phase ^= 4u << x;
+          fly &= ~(4u << x);
+          const unsigned char* from = smem + kSmemRaw + gi * kRaw + kRawK;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {  // i = 2 jj + half
-            uint4 w = vr[x][i];
-            if (!cur[x]) w = make_uint4(0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u);  // codes 0
+            const uint4 w = *reinterpret_cast<const uint4*>(from + i * 512 + lane * 16);
             unsigned char* d2 = dst + 8 * (i >> 1) * kVSbo + 64 * (i & 1);
             *reinterpret_cast<uint2*>(d2) = make_uint2(i8_lo2(w.x), i8_hi2(w.x));
             *reinterpret_cast<uint2*>(d2 + 16) = make_uint2(i8_lo2(w.y), i8_hi2(w.y));
@@ -478,131 +657,117 @@ __global__ void __launch_bounds__(kThreads, 1)
             *reinterpret_cast<uint2*>(d2 + 48) = make_uint2(i8_lo2(w.w), i8_hi2(w.w));
           }
         } else {
-          // four tokens' rows of 8 channels, twice; a token with a non-finite value anywhere is left out as a whole
+          // window tokens, zeros behind the last and in the place of what is not finite
+          const int upto = p0 >= nc ? end : 0;
 #pragma unroll 1
-          for (int pass = 0; pass < 2; ++pass) {
-#pragma unroll 1
-            for (int jj = 0; jj < 2; ++jj) {
-              uint32_t w[4][4];
+          for (int i = 0; i < 8; ++i) {
+            const int t = i & 3, pos = p0 + 4 * t4 + t;
+            uint4 a = make_uint4(0, 0, 0, 0);
+            if (pos < upto) a = *reinterpret_cast<const uint4*>(wv + (size_t)(pos % C.ring) * D + 64 * (i >> 2) + 8 * g8);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+            unsigned char* d2 = dst + 8 * (i >> 2) * kVSbo + 2 * t;
 #pragma unroll
-              for (int t = 0; t < 4; ++t) {
-                const int p = p0 + 4 * t4 + t;
-                uint4 a = make_uint4(0, 0, 0, 0);
-                if (p < end && !(pass && (bad >> (4 * t4 + t) & 1)))
-                  a = *reinterpret_cast<const uint4*>(C.win_v + (((size_t)b * P.hkv + g) * C.ring + p % C.ring) * D + 64 * jj + 8 * g8);
-                w[t][0] = a.x, w[t][1] = a.y, w[t][2] = a.z, w[t][3] = a.w;
-                if (pass == 0) {
-                  bool nf = false;
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)
-                    nf |= (w[t][e] & 0x7c00u) == 0x7c00u || (w[t][e] & 0x7c000000u) == 0x7c000000u;
-                  if (nf) bad |= 1u << (4 * t4 + t);
-                }
-              }
-              if (pass == 1) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const uint32_t sel = e & 1 ? 0x7632 : 0x5410;
-                  *reinterpret_cast<uint2*>(dst + 8 * jj * kVSbo + 16 * e) =
-                      make_uint2(__byte_perm(w[0][e >> 1], w[1][e >> 1], sel), __byte_perm(w[2][e >> 1], w[3][e >> 1], sel));
-                }
-              }
+            for (int e = 0; e < 8; ++e) {
+              const uint32_t y = w[e >> 1] >> 16 * (e & 1) & 0xffffu;
+              *reinterpret_cast<unsigned short*>(d2 + 16 * e) = (unsigned short)((y & 0x7c00u) == 0x7c00u ? 0 : y);
             }
-            if (pass == 0) bad = __reduce_or_sync(0xffffffffu, bad);
           }
-        }
-        if (lane == 0) {
-          sh.scale[st][gi] = cur[x] ? csc[x] : make_float2(1.f, win ? 1.f : 0.f);
-          sh.bad[st][gi] = bad;
-          const bool there = cur[x] || win;
-          if (there) atomicOr(&sh.live[st], 1u << gi);
-          else atomicAnd(&sh.live[st], ~(1u << gi));
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.vfull[st]);
+      if (lane == 0) mbar_arrive(&sh.vfull);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        next_values(x, in[x]);
+        in[x] = ik[x];
+      }
+      if (j + 2 < j1 && !failed) store_keys(j + 2);
     }
     if (failed) {
       if (lane == 0) atomicOr(&g_int8_prefill_err, TQ_DEVERR_TIMEOUT);
-      sh.fail = 1;
+      for (int x = 0; x < 2; ++x) {  // copies in flight land before the block's memory is given up
+        if (fly >> x & 1) (void)mbar_wait(&sh.rawk[cw + 4 * x], phase >> x & 1);
+        if (fly >> (2 + x) & 1) (void)mbar_wait(&sh.rawv[cw + 4 * x], phase >> (2 + x) & 1);
+      }
     }
   } else {
     // ------------------------------------------------------------ products
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 32;");
-    if (warp == 12 && lane == 0 && j1 > j0) {
+    if (lane == 0 && j1 > j0) {
       const uint64_t dq = tc_desc(sbase + kSmemQ, kQLbo, kQSbo);
       bool ok = true;
-      auto scores = [&](int u, int st) {  // S of unit u from the keys in stage st
+      auto scores = [&](int u, int st) {
         const uint64_t dk = tc_desc(sbase + kSmemK + st * kKTile, kKLbo, kKSbo);
 #pragma unroll
         for (int ql = 0; ql < QL; ++ql) {
           const uint64_t da = dq + (uint64_t)(((RT == 2 ? u : ql) * kQTile) >> 4);
-#pragma unroll 1
+#pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            mma_ss(tmem + 128u * u, da + (uint64_t)(2 * kQLbo >> 4) * k, dk + (uint64_t)(2 * kKLbo >> 4) * k, ql > 0 || k > 0);
+            mma_ss(tmem + 128u * u, da + (uint64_t)((2 * kQLbo >> 4) * k), dk + (uint64_t)((2 * kKLbo >> 4) * k), ql > 0 || k > 0);
         }
         tc_commit(&sh.sfull[u]);
       };
-      auto values = [&](int u, int st) {  // O of unit u: 8 k-steps of 16 tokens, hi and lo limbs
-        const uint64_t dv = tc_desc(sbase + kSmemV + st * kVTile, kVLbo, kVSbo);
+      auto values = [&](int u, bool fresh) {  // O of unit u: 8 k-steps of 16 tokens, lo and hi limbs
+        const uint64_t dv = tc_desc(sbase + kSmemV, kVLbo, kVSbo);
         const uint32_t a = tmem + 128u * u, d = tmem + 256u + 128u * u;
-#pragma unroll 1
+#pragma unroll
         for (int k = 0; k < KT / 16; ++k) {
-          mma_ts(d, a + 16u * k + 8u, dv + (uint64_t)(2 * kVLbo >> 4) * k, k > 0);
-          mma_ts(d, a + 16u * k, dv + (uint64_t)(2 * kVLbo >> 4) * k, 1);
+          mma_ts(d, a + 16u * k + 8u, dv + (uint64_t)((2 * kVLbo >> 4) * k), k > 0 || !fresh);
+          mma_ts(d, a + 16u * k, dv + (uint64_t)((2 * kVLbo >> 4) * k), 1);
         }
         tc_commit(&sh.ofull[u]);
       };
-      // tile of unit u's step i: RT = 2 both units take every tile, RT = 1 they take turns
+      // one wait and its fence
+      auto need = [&](uint64_t* bar, uint32_t parity) {
+        ok = ok && mbar_wait(bar, parity);
+        tc_after();
+      };
       if (RT == 2) {
-        ok = mbar_wait(&sh.kfull[0], 0);
+        // both units take every tile
+        need(&sh.kfull[0], 0);
         if (ok) {
-          tc_after();
           scores(0, 0);
           scores(1, 0);
           tc_commit(&sh.kfree[0]);
         }
         for (int j = j0; ok && j < j1; ++j) {
-          const int i = j - j0, st = i & 1, sp = (i >> 1) & 1, nst = (i + 1) & 1, nsp = ((i + 1) >> 1) & 1;
+          const int i = j - j0, nst = (i + 1) & 1;
+          need(&sh.vfull, i & 1);
 #pragma unroll 1
-          for (int u = 0; ok && u < 2; ++u) {
-            ok = mbar_wait(&sh.pready[u], i & 1) && mbar_wait(&sh.vfull[st], sp);
+          for (int u = 0; u < 2; ++u) {
+            need(&sh.pready[u], i & 1);
             if (!ok) break;
-            tc_after();
-            values(u, st);
-            if (u == 1) tc_commit(&sh.vfree[st]);
+            values(u, i % kRun == 0);
+            if (u == 1) tc_commit(&sh.vfree);
             if (j + 1 < j1) {
-              ok = mbar_wait(&sh.kfull[nst], nsp);
+              need(&sh.kfull[nst], ((i + 1) >> 1) & 1);
               if (!ok) break;
-              tc_after();
               scores(u, nst);
               if (u == 1) tc_commit(&sh.kfree[nst]);
             }
           }
         }
       } else {
-        for (int i = 0; ok && i < min(2, j1 - j0); ++i) {
-          ok = mbar_wait(&sh.kfull[i], 0);
-          if (!ok) break;
-          tc_after();
-          scores(i, i);
-          tc_commit(&sh.kfree[i]);
+        // they take turns: S of the next tile (the other unit's) runs during this tile's softmax
+        need(&sh.kfull[0], 0);
+        if (ok) {
+          scores(0, 0);
+          tc_commit(&sh.kfree[0]);
         }
         for (int j = j0; ok && j < j1; ++j) {
-          const int i = j - j0, u = i & 1, sp = (i >> 1) & 1;
-          ok = mbar_wait(&sh.pready[u], sp) && mbar_wait(&sh.vfull[u], sp);
-          if (!ok) break;
-          tc_after();
-          values(u, u);
-          tc_commit(&sh.vfree[u]);
-          if (j + 2 < j1) {
-            ok = mbar_wait(&sh.kfull[u], sp ^ 1);
+          const int i = j - j0, u = i & 1;
+          if (j + 1 < j1) {
+            // (the other unit's last P was read by products issued before)
+            need(&sh.kfull[u ^ 1], ((i + 1) >> 1) & 1);
             if (!ok) break;
-            tc_after();
-            scores(u, u);
-            tc_commit(&sh.kfree[u]);
+            scores(u ^ 1, u ^ 1);
+            tc_commit(&sh.kfree[u ^ 1]);
           }
+          need(&sh.vfull, i & 1);
+          need(&sh.pready[u], (i >> 1) & 1);
+          if (!ok) break;
+          values(u, (i >> 1) % kRun == 0);
+          tc_commit(&sh.vfree);
         }
       }
       // tensor memory is given back and the operands' memory reused only when every product has ended
@@ -610,8 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!mbar_wait(&sh.drained, 0)) ok = false;
       if (!ok) {
         atomicOr(&g_int8_prefill_err, TQ_DEVERR_TIMEOUT);
-        sh.fail = 1;
-      }
+        }
     }
     __syncwarp();
   }
@@ -625,6 +789,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Rows of a block's query tile: two tiles of 128.
 bool int8_prefill_tc_ok(const KParams& P, int n_query) { return P.d == D && (long long)n_query * P.G > 16; }
+
+// Blocks' rows a KV head, and the places of the gathered sums (afrag) and of the partial results in `splits` splits;
+// returns the bytes they take.
+static size_t places(const KParams& P, int batch, int n_query, int splits, bool one, WsLayout* L) {
+  const int S = one ? 2 * splits : splits, per = one ? 128 : 256;
+  const size_t heads = (size_t)batch * n_query * P.hq;
+  const size_t blocks = ((size_t)n_query * P.G + per - 1) / per * P.hkv * batch * splits;
+  L->n_comp_splits = splits;
+  L->afrag = 0;
+  size_t o = blocks * 256 * D * sizeof(float);
+  L->ml = o;
+  if (S > 1) o += (heads * S * 2 * sizeof(float) + 255) & ~(size_t)255;
+  L->acc = o;
+  if (S > 1) o += (heads * S * (size_t)D * sizeof(float) + 255) & ~(size_t)255;
+  return o;
+}
 
 // Splits of the key tiles: blocks are one to an SM, so the count whose last wave is fullest, at least four tiles
 // a split; the joining costs a pass over the partial outputs (about 3 % of a block's work a split).
@@ -644,16 +824,9 @@ WsLayout int8_prefill_layout(const KParams& P, int batch, int n_query, int max_c
     }
   }
   WsLayout L{};
-  L.n_comp_splits = best;
-  const size_t heads = (size_t)batch * n_query * P.hq;
-  size_t o = 0;
-  if (best > 1) {
-    L.ml = o;
-    o += (heads * best * 2 * sizeof(float) + 255) & ~(size_t)255;
-    L.acc = o;
-    o += (heads * best * (size_t)D * sizeof(float) + 255) & ~(size_t)255;
-  }
-  L.total = std::max<size_t>(o, 256);
+  // room for either kind of block: the queries' type is not known here
+  const size_t one = places(P, batch, n_query, best, true, &L);
+  L.total = std::max(one, places(P, batch, n_query, best, false, &L));
   return L;
 }
 
@@ -667,10 +840,14 @@ cudaError_t launch_int8_prefill(const KParams& P, const KCache& C, int n_query, 
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
   const int per = one ? 128 : 256;
+  WsLayout K{}, J;
+  places(P, C.batch, n_query, L.n_comp_splits, one, &K);
+  J = K;  // the joining kernel's splits
+  J.n_comp_splits = one ? 2 * L.n_comp_splits : L.n_comp_splits;
   kern<<<dim3((rows + per - 1) / per, P.hkv, C.batch * L.n_comp_splits), kThreads, kSmemBytes, st>>>(P, C, n_query, q, dtype, scale,
-                                                                                                 out, lse, w, L, max_ctx);
-  if ((e = cudaGetLastError()) != cudaSuccess || L.n_comp_splits == 1) return e;
-  return launch_int8_combine(P, w, L, (long long)C.batch * n_query, out, lse, st);
+                                                                                                 out, lse, w, K, max_ctx);
+  if ((e = cudaGetLastError()) != cudaSuccess || J.n_comp_splits == 1) return e;
+  return launch_int8_combine(P, w, J, (long long)C.batch * n_query, true, out, lse, st);
 }
 
 cudaError_t read_clear_int8_prefill_error(unsigned* bits) {
