@@ -10,10 +10,10 @@
 // ride on the weights relative to a power of two that bounds the scales seen so far, adjusted with
 // the running maximum.
 //
-// The page holds its codes in operand order, so a lane's 16-byte load is four operands and the
-// scores come out of the first product in the layout the second one takes them: a warp carries a page
-// from load to accumulator in registers, without shared memory and without another warp.  Warps take
-// the pages (16 tokens; the window in groups of 16) of their split in turn and meet once at the end.
+// The page holds its codes in operand order, so a lane's 16 bytes are four operands and the scores come out
+// of the first product in the layout the second one takes them: a warp carries a page from its codes to the
+// accumulators without another warp.  Warps take the pages (16 tokens; the window in groups of 16) of their
+// split in turn, each through its own ring of bulk copies, and meet once at the end.
 #include <math.h>
 
 #include <algorithm>
@@ -32,7 +32,9 @@ constexpr int kThreads = 32 * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kWeightTop = 16384.f;  // f16 weights reach up to this: lo limbs stay normal down to 2^-26 of the top
 
-__host__ __device__ constexpr int ctas_per_sm(int d) { return d == 128 ? 3 : 2; }
+__host__ __device__ constexpr int ctas_per_sm(int d) { return d == 128 ? 4 : 2; }
+__host__ __device__ constexpr int raw_bytes(int d) { return 32 * d + kI8Head; }  // a page's scales and codes
+constexpr int kRing = 3;  // pages in flight a warp
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -53,6 +55,19 @@ __device__ __forceinline__ void split2(float a, float b, uint32_t& hi, uint32_t&
   lo = *reinterpret_cast<const uint32_t*>(&l);
 }
 
+__device__ __forceinline__ uint32_t smem_u32(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+// Bounded wait (about a second): false when it ran out.
+__device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity) {
+  uint32_t done = 0;
+  for (unsigned it = 0; it < (1u << 20) && !done; ++it)
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(done)
+        : "r"(smem_u32(b)), "r"(parity), "n"(1000)
+        : "memory");
+  return done != 0;
+}
+
 // Smallest power of two >= s (s a page scale: 0 or normal)
 __device__ __forceinline__ float pow2_above(float s) {
   return __uint_as_float((__float_as_uint(s) + 0x007fffffu) & 0x7f800000u);
@@ -61,16 +76,18 @@ __device__ __forceinline__ float pow2_above(float s) {
 // 1 / v for a power of two v between 2^-126 and 2^126
 __device__ __forceinline__ float pow2_inv(float v) { return __uint_as_float(0x7f000000u - __float_as_uint(v)); }
 
+template <int D>
 struct Shared {
-  uint4 afr[16][32];      // query operand: k-step, lane
+  uint4 afr[D / 16][32];  // query operand: k-step, lane
   float unscale[8];       // 1 / the power of two of a query row
   float m[kWarps][8], l[kWarps][8];
+  uint64_t full[kWarps][kRing];
 };
 
 // Row scale (a power of two that brings the largest magnitude into [2^13, 2^14)) and operand fragments of
 // the G query rows at q [G][dh].  All threads; ends with a barrier.
 template <int D>
-__device__ void load_query(Shared& sh, const void* q, int dtype, size_t row0, int G, int dh) {
+__device__ void load_query(Shared<D>& sh, const void* q, int dtype, size_t row0, int G, int dh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int h = warp; h < 8; h += kWarps) {
     float a = 0.f;
@@ -107,15 +124,13 @@ struct Items {
 };
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) i8_decode_kernel(const __grid_constant__ KParams P,
-                                                             const __grid_constant__ KCache C, const void* q, int dtype,
-                                                             float scale, const int32_t* __restrict__ pages,
-                                                             const int32_t* __restrict__ counts, int n_sel, float* out,
-                                                             float* lse, float* scores, unsigned char* ws, WsLayout L,
-                                                             int max_ctx) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
+    i8_decode_kernel(const __grid_constant__ KParams P, const __grid_constant__ KCache C, const void* q, int dtype,
+                     float scale, const int32_t* __restrict__ pages, const int32_t* __restrict__ counts, int n_sel,
+                     float* out, float* lse, float* scores, unsigned char* ws, WsLayout L, int max_ctx) {
   constexpr int J = D / 64;
-  __shared__ Shared sh;
-  extern __shared__ __align__(16) float merge[];  // [kWarps][8][D]
+  __shared__ Shared<D> sh;
+  extern __shared__ __align__(128) unsigned char dyn[];  // [kWarps][kRing] pages, at the end [kWarps][8][D] floats
   const int s = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
   const int G = P.G, S = L.n_comp_splits;
@@ -154,9 +169,47 @@ __global__ void __launch_bounds__(kThreads) i8_decode_kernel(const __grid_consta
   }
   if (bad && tid == 0) atomicOr(&g_int8_decode_err, TQ_DEVERR_SEQ_LEN);
   it.total = it.pages + (nwin + kPage - 1) / kPage;
-  // the split's share, in whole rounds of the warps where there are enough
   const int per = (it.total + S - 1) / S;
-  const int i0 = min(it.total, s * per), i1 = min(it.total, i0 + per);
+  const int i0 = min(it.total, s * per), i1 = min(it.total, i0 + per), ip = min(i1, it.pages);  // pages [i0, ip)
+
+  // this warp's pages: i0 + warp + kWarps k, k < mine; lane k % 32 knows page k's place in the pool and its ordinal
+  const int mine = max(0, (ip - i0 - warp + kWarps - 1) / kWarps);
+  unsigned char* ring = dyn + (size_t)warp * kRing * raw_bytes(D);
+  int ord = 0;
+  long long pid = -1;
+  auto look_up = [&](int k0, int& o, long long& p) {
+    p = -1;
+    if (k0 + lane < mine) {
+      const int i = i0 + warp + kWarps * (k0 + lane);
+      o = it.list ? it.list[i] : i;
+      if (o >= 0 && o < np) p = C.block_table[(size_t)cb * C.max_pages + o];
+      if (p < 0 || p >= C.n_pages) {
+        atomicOr(&g_int8_decode_err, TQ_DEVERR_PAGE_INDEX);
+        p = -1;
+      }
+    }
+  };
+  auto fetch = [&](long long p, int slot) {  // one lane
+    const uint32_t bar = smem_u32(&sh.full[warp][slot]);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(raw_bytes(D)) : "memory");
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_u32(ring + slot * raw_bytes(D))),
+                 "l"(i8_subblock(P, C, p, g) + i8_off_head(D)), "r"(raw_bytes(D)), "r"(bar)
+                 : "memory");
+  };
+  if (lane == 0) {
+    for (int i = 0; i < kRing; ++i)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&sh.full[warp][i])) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  look_up(0, ord, pid);
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < kRing; ++k) {
+    const long long p = __shfl_sync(0xffffffffu, pid, k);
+    if (lane == 0 && k < mine && p >= 0) fetch(p, k);
+  }
 
   load_query<D>(sh, q, dtype, head0, G, P.dh);
   const float qs = sh.unscale[g8] * scale;
@@ -172,59 +225,9 @@ __global__ void __launch_bounds__(kThreads) i8_decode_kernel(const __grid_consta
         for (int r = 0; r < 4; ++r) acc[j][h][i][r] = 0.f;
   float m = -INFINITY, l = 0.f, vref = 0.f;  // of head g8 (l: this lane's tokens)
 
-  for (int i = i0 + warp; i < i1; i += kWarps) {
-    const bool is_page = i < it.pages;
-    float sacc[2][4] = {};
-    float ks = 1.f, vs = 1.f;
-    int pos0, live_to;  // position of the group's first token; tokens at positions < live_to count
-    const unsigned char* sb = nullptr;
-    if (is_page) {
-      const int ord = it.list ? it.list[i] : i;
-      long long page = -1;
-      if (ord >= 0 && ord < np) page = C.block_table[(size_t)cb * C.max_pages + ord];
-      if (page < 0 || page >= C.n_pages) {
-        if (lane == 0) atomicOr(&g_int8_decode_err, TQ_DEVERR_PAGE_INDEX);
-        continue;
-      }
-      sb = i8_subblock(P, C, page, g);
-      pos0 = ord * kPage;
-      live_to = it.nc;
-      const float2 sc = *reinterpret_cast<const float2*>(sb + i8_off_head(D));
-      ks = sc.x;
-      vs = sc.y;
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const uint4 w = *reinterpret_cast<const uint4*>(sb + i8_off_kcodes(D) + nt * 8 * D + j * 512 + lane * 16);
-          mma16816(sacc[nt], sh.afr[4 * j][lane], i8_lo2(w.x), i8_hi2(w.x));
-          mma16816(sacc[nt], sh.afr[4 * j + 1][lane], i8_lo2(w.y), i8_hi2(w.y));
-          mma16816(sacc[nt], sh.afr[4 * j + 2][lane], i8_lo2(w.z), i8_hi2(w.z));
-          mma16816(sacc[nt], sh.afr[4 * j + 3][lane], i8_lo2(w.w), i8_hi2(w.w));
-        }
-    } else {
-      pos0 = it.nc + (i - it.pages) * kPage;
-      live_to = it.nc + nwin;
-      const __half* ring = C.win_k + ((size_t)cb * P.hkv + g) * C.ring * D;
-#pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        const int pos = pos0 + 4 * (g8 >> 1) + 2 * nt + (g8 & 1);
-        const __half* row = ring + (size_t)(pos % C.ring) * D + 16 * t4;
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;  // rows that are not there may hold anything
-          if (pos < live_to) {
-            w0 = *reinterpret_cast<const uint4*>(row + 64 * j);
-            w1 = *reinterpret_cast<const uint4*>(row + 64 * j + 8);
-          }
-          mma16816(sacc[nt], sh.afr[4 * j][lane], w0.x, w0.y);
-          mma16816(sacc[nt], sh.afr[4 * j + 1][lane], w0.z, w0.w);
-          mma16816(sacc[nt], sh.afr[4 * j + 2][lane], w1.x, w1.y);
-          mma16816(sacc[nt], sh.afr[4 * j + 3][lane], w1.z, w1.w);
-        }
-      }
-    }
-    // scores of head g8, tokens 4 t4 + 2 nt + e
+  // scores -> weights in operand order; the running state and the accumulators follow
+  auto softmax = [&](const float (&sacc)[2][4], float ks, float vs, int pos0, int live_to) -> uint4 {
+    // head g8, tokens 4 t4 + 2 nt + e
     float x[2][2], mx = -INFINITY;
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
@@ -269,19 +272,103 @@ __global__ void __launch_bounds__(kThreads) i8_decode_kernel(const __grid_consta
     uint4 a;
     split2(p[0][0] * wv, p[0][1] * wv, a.x, a.y);
     split2(p[1][0] * wv, p[1][1] * wv, a.z, a.w);
-    if (is_page) {
+    return a;
+  };
+
+  bool failed = false;
+  uint32_t fly = 0;  // slots with a copy in flight (this warp's next phases)
+  uint32_t phase = 0;
+  int slot = 0;
+#pragma unroll
+  for (int k = 0; k < kRing; ++k)
+    if (k < mine && __shfl_sync(0xffffffffu, pid, k) >= 0) fly |= 1u << k;
+  int nord = 0;
+  long long npid = -1;
+#pragma unroll 1
+  for (int k = 0; k < mine; ++k) {
+    const int k32 = k & 31;
+    if (k32 == 32 - kRing) look_up((k & ~31) + 32, nord, npid);  // the next 32, before the copies ahead reach them
+    const long long p = __shfl_sync(0xffffffffu, pid, k32);
+    const int o = __shfl_sync(0xffffffffu, ord, k32);
+    if (p >= 0) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[warp][slot], phase >> slot & 1))) {
+        failed = true;
+        break;
+      }
+      phase ^= 1u << slot;
+      fly &= ~(1u << slot);
+      const unsigned char* sb = ring + slot * raw_bytes(D);
+      const float2 sc = *reinterpret_cast<const float2*>(sb);
+      float sacc[2][4] = {};
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const uint4 w = *reinterpret_cast<const uint4*>(sb + kI8Head + nt * 8 * D + j * 512 + lane * 16);
+          mma16816(sacc[nt], sh.afr[4 * j][lane], i8_lo2(w.x), i8_hi2(w.x));
+          mma16816(sacc[nt], sh.afr[4 * j + 1][lane], i8_lo2(w.y), i8_hi2(w.y));
+          mma16816(sacc[nt], sh.afr[4 * j + 2][lane], i8_lo2(w.z), i8_hi2(w.z));
+          mma16816(sacc[nt], sh.afr[4 * j + 3][lane], i8_lo2(w.w), i8_hi2(w.w));
+        }
+      const uint4 a = softmax(sacc, sc.x, sc.y, o * kPage, it.nc);
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint4 w = *reinterpret_cast<const uint4*>(sb + i8_off_vcodes(D) + j * 1024 + h * 512 + lane * 16);
+          const uint4 w = *reinterpret_cast<const uint4*>(sb + kI8Head + 16 * D + j * 1024 + h * 512 + lane * 16);
           mma16816(acc[j][h][0], a, i8_lo2(w.x), i8_hi2(w.x));
           mma16816(acc[j][h][1], a, i8_lo2(w.y), i8_hi2(w.y));
           mma16816(acc[j][h][2], a, i8_lo2(w.z), i8_hi2(w.z));
           mma16816(acc[j][h][3], a, i8_lo2(w.w), i8_hi2(w.w));
         }
-    } else {
-      const __half* ring = C.win_v + ((size_t)cb * P.hkv + g) * C.ring * D;
+      __syncwarp();  // every lane has read the slot
+    }
+    // the page kRing on takes this one's slot
+    const int ka = k + kRing;
+    const long long pn = __shfl_sync(0xffffffffu, (ka ^ k) & 32 ? npid : pid, ka & 31);
+    if (ka < mine && pn >= 0) {
+      if (lane == 0) fetch(pn, slot);
+      fly |= 1u << slot;
+    }
+    slot = slot + 1 == kRing ? 0 : slot + 1;
+    if (k32 == 31) {
+      pid = npid;
+      ord = nord;
+    }
+  }
+  if (failed) {
+    if (lane == 0) atomicOr(&g_int8_decode_err, TQ_DEVERR_TIMEOUT);
+    for (int i = 0; i < kRing; ++i)  // copies in flight land before the block's memory is given up
+      if (fly >> i & 1) (void)mbar_wait(&sh.full[warp][i], phase >> i & 1);
+  }
+  // window groups [max(i0, pages), i1), counted on after the pages so that the warps' shares stay even
+  {
+    const int w0 = max(i0, it.pages);
+    int i = w0 + (warp + kWarps - (w0 - i0) % kWarps) % kWarps;
+#pragma unroll 1
+    for (; i < i1; i += kWarps) {
+      const int pos0 = it.nc + (i - it.pages) * kPage, live_to = it.nc + nwin;
+      const __half* kring = C.win_k + ((size_t)cb * P.hkv + g) * C.ring * D;
+      float sacc[2][4] = {};
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt) {
+        const int pos = pos0 + 4 * (g8 >> 1) + 2 * nt + (g8 & 1);
+        const __half* row = kring + (size_t)(pos % C.ring) * D + 16 * t4;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+          uint4 w0 = make_uint4(0, 0, 0, 0), w1 = w0;  // rows that are not there may hold anything
+          if (pos < live_to) {
+            w0 = *reinterpret_cast<const uint4*>(row + 64 * j);
+            w1 = *reinterpret_cast<const uint4*>(row + 64 * j + 8);
+          }
+          mma16816(sacc[nt], sh.afr[4 * j][lane], w0.x, w0.y);
+          mma16816(sacc[nt], sh.afr[4 * j + 1][lane], w0.z, w0.w);
+          mma16816(sacc[nt], sh.afr[4 * j + 2][lane], w1.x, w1.y);
+          mma16816(sacc[nt], sh.afr[4 * j + 3][lane], w1.z, w1.w);
+        }
+      }
+      const uint4 a = softmax(sacc, 1.f, 1.f, pos0, live_to);
+      const __half* vring = C.win_v + ((size_t)cb * P.hkv + g) * C.ring * D;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         uint32_t r[4][4];
@@ -289,7 +376,7 @@ __global__ void __launch_bounds__(kThreads) i8_decode_kernel(const __grid_consta
         for (int t = 0; t < 4; ++t) {
           const int pos = pos0 + 4 * t4 + t;
           uint4 w = make_uint4(0, 0, 0, 0);
-          if (pos < live_to) w = *reinterpret_cast<const uint4*>(ring + (size_t)(pos % C.ring) * D + 64 * j + 8 * g8);
+          if (pos < live_to) w = *reinterpret_cast<const uint4*>(vring + (size_t)(pos % C.ring) * D + 64 * j + 8 * g8);
           r[t][0] = w.x, r[t][1] = w.y, r[t][2] = w.z, r[t][3] = w.w;
         }
 #pragma unroll
@@ -308,14 +395,16 @@ __global__ void __launch_bounds__(kThreads) i8_decode_kernel(const __grid_consta
     sh.l[warp][g8] = l;
   }
   const float unit = vref * (1.f / kWeightTop);
-  float* mine = merge + ((size_t)warp * 8 + g8) * D;
+  float* merge = reinterpret_cast<float*>(dyn);
+  __syncthreads();  // every warp's ring is idle
+  float* box = merge + ((size_t)warp * 8 + g8) * D;
 #pragma unroll
   for (int j = 0; j < J; ++j)
 #pragma unroll
     for (int c = 0; c < 2; ++c)  // column 2 t4 + c: dims 64 j + 16 t4 + 8 c + 4 h + i
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<float4*>(mine + 64 * j + 16 * t4 + 8 * c + 4 * h) =
+        *reinterpret_cast<float4*>(box + 64 * j + 16 * t4 + 8 * c + 4 * h) =
             make_float4((acc[j][h][0][c] + acc[j][h][0][c + 2]) * unit, (acc[j][h][1][c] + acc[j][h][1][c + 2]) * unit,
                         (acc[j][h][2][c] + acc[j][h][2][c + 2]) * unit, (acc[j][h][3][c] + acc[j][h][3][c + 2]) * unit);
   __syncthreads();
@@ -380,11 +469,13 @@ template <int D>
 cudaError_t decode(const KParams& P, const KCache& C, const void* q, int dtype, float scale, const int32_t* pages,
                    const int32_t* counts, int n_sel, float* out, float* lse, float* scores, unsigned char* ws,
                    const WsLayout& L, int max_ctx, cudaStream_t st) {
-  const size_t dyn = (size_t)kWarps * 8 * D * sizeof(float);
+  const size_t dyn = std::max((size_t)kWarps * kRing * raw_bytes(D), (size_t)kWarps * 8 * D * sizeof(float));
+  cudaError_t e = cudaFuncSetAttribute(i8_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn);
+  if (e != cudaSuccess) return e;
   const dim3 grid(L.n_comp_splits, P.hkv, C.batch);
   i8_decode_kernel<D><<<grid, kThreads, dyn, st>>>(P, C, q, dtype, scale, pages, counts, n_sel, out, lse, scores, ws, L,
                                                    max_ctx);
-  cudaError_t e = cudaGetLastError();
+  e = cudaGetLastError();
   if (e != cudaSuccess || L.n_comp_splits == 1) return e;
   return launch_int8_combine(P, ws, L, C.batch, false, out, lse, st);
 }

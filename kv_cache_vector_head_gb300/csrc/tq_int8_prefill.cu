@@ -138,10 +138,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
 __device__ __forceinline__ float pow2_above(float s) { return __uint_as_float((__float_as_uint(s) + 0x007fffffu) & 0x7f800000u); }
 __device__ __forceinline__ float pow2_inv(float v) { return __uint_as_float(0x7f000000u - __float_as_uint(v)); }
 
