@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kWeightTop = 16384.f;  // f16 weights reach up to this: lo limbs stay normal down to 2^-26 of the top
 
 __host__ __device__ constexpr int ctas_per_sm(int d) { return d == 128 ? 4 : 2; }
@@ -68,6 +68,12 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* b, uint32_t parity) {
   return done != 0;
 }
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Smallest power of two >= s (s a page scale: 0 or normal)
 __device__ __forceinline__ float pow2_above(float s) {
   return __uint_as_float((__float_as_uint(s) + 0x007fffffu) & 0x7f800000u);
@@ -96,9 +102,10 @@ __device__ void load_query(Shared<D>& sh, const void* q, int dtype, size_t row0,
     a = warp_max_f(a);
     // 2^(13 - floor(log2 a)); the exponent is kept where both it and its reciprocal are normal
     const int e = a > 0.f ? min(max(140 - (int)(__float_as_uint(a) >> 23), -113), 126) : 0;
+    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
     if (lane == 0) {
       sh.unscale[h] = __uint_as_float((uint32_t)(127 - e) << 23);
-      sh.m[0][h] = __uint_as_float((uint32_t)(127 + e) << 23);
+      sh.m[0][h] = up;
     }
   }
   __syncthreads();
@@ -117,11 +124,34 @@ __device__ void load_query(Shared<D>& sh, const void* q, int dtype, size_t row0,
   __syncthreads();
 }
 
-// Work of one (sequence, KV head): pages first, then the window in groups of 16.
+// Work of one (sequence, KV head): its pages (all in order, or a list's), then the window in groups of 16.
 struct Items {
-  int n, nc, pages, total;
-  const int32_t* list;  // page ordinals to take, or null: all pages in order
+  int n, nc, np, nwin, pages, total;
+  bool bad;
 };
+
+__device__ __forceinline__ Items items_of(const KCache& C, int hkv, const int32_t* counts, int n_sel, int max_ctx, int b, int g) {
+  Items it;
+  it.n = C.seq_len[b];
+  it.nc = C.n_compressed[b];
+  it.bad = it.n < 0 || it.n > max_ctx || it.nc < 0 || it.nc > it.n;
+  it.n = min(max(it.n, 0), max_ctx);
+  it.nc = min(max(it.nc, 0), it.n);
+  it.np = (it.nc + kPage - 1) / kPage;
+  it.nwin = it.n - it.nc;
+  // positions from nc on are in the ring; a virtual sequence's nc is its parent's clipped to what it sees
+  it.bad |= it.np > C.max_pages || it.nwin >= C.ring;
+  it.np = min(it.np, C.max_pages);
+  it.nwin = min(it.nwin, C.ring - 1);
+  it.pages = it.np;
+  if (counts) {
+    it.pages = counts[(size_t)b * hkv + g];
+    it.bad |= it.pages < 0 || it.pages > n_sel;
+    it.pages = min(max(it.pages, 0), n_sel);
+  }
+  it.total = it.pages + (it.nwin + kPage - 1) / kPage;
+  return it;
+}
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
@@ -131,88 +161,66 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
   constexpr int J = D / 64;
   __shared__ Shared<D> sh;
   extern __shared__ __align__(128) unsigned char dyn[];  // [kWarps][kRing] pages, at the end [kWarps][8][D] floats
-  const int s = blockIdx.x, g = blockIdx.y, b = blockIdx.z;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
   const int G = P.G, S = L.n_comp_splits;
+  unsigned char* ring = dyn + (size_t)warp * kRing * raw_bytes(D);
+  if (lane == 0) {
+    for (int i = 0; i < kRing; ++i)
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&sh.full[warp][i])) : "memory");
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  bool failed = false;
+  uint32_t fly = 0, phase = 0;  // bit: a copy is in flight into the slot; the parity it ends
+  int slot = 0;
+
+  const int b = blockIdx.z, g = blockIdx.y, s = blockIdx.x;
   const size_t head0 = (size_t)b * P.hq + (size_t)g * G;
   const int cb = C.parent ? C.parent[b] : b;
-
-  Items it;
-  it.n = C.seq_len[b];
-  it.nc = C.n_compressed[b];
-  bool bad = false;
-  if (it.n < 0 || it.n > max_ctx || it.nc < 0 || it.nc > it.n) {
-    bad = true;
-    it.n = min(max(it.n, 0), max_ctx);
-    it.nc = min(max(it.nc, 0), it.n);
-  }
-  int np = (it.nc + kPage - 1) / kPage;
-  if (np > C.max_pages) {
-    bad = true;
-    np = C.max_pages;
-  }
-  int nwin = it.n - it.nc;
-  // positions from nc on are in the ring; a virtual sequence's nc is its parent's clipped to what it sees
-  if (nwin >= C.ring) {
-    bad = true;
-    nwin = C.ring - 1;
-  }
-  it.pages = np;
-  it.list = nullptr;
-  if (pages) {
-    it.list = pages + ((size_t)b * P.hkv + g) * n_sel;
-    it.pages = counts[(size_t)b * P.hkv + g];
-    if (it.pages < 0 || it.pages > n_sel) {
-      bad = true;
-      it.pages = min(max(it.pages, 0), n_sel);
-    }
-  }
-  if (bad && tid == 0) atomicOr(&g_int8_decode_err, TQ_DEVERR_SEQ_LEN);
-  it.total = it.pages + (nwin + kPage - 1) / kPage;
-  const int per = (it.total + S - 1) / S;
-  const int i0 = min(it.total, s * per), i1 = min(it.total, i0 + per), ip = min(i1, it.pages);  // pages [i0, ip)
+  const Items it = items_of(C, P.hkv, counts, n_sel, max_ctx, b, g);
+  if (it.bad && s == 0 && tid == 0) atomicOr(&g_int8_decode_err, TQ_DEVERR_SEQ_LEN);
+  const int per = (it.total + S - 1) / S, i0 = min(it.total, s * per), i1 = min(it.total, i0 + per);
+  const int32_t* list = pages ? pages + ((size_t)b * P.hkv + g) * n_sel : nullptr;
+  const int ip = min(i1, it.pages);  // pages [i0, ip)
 
   // this warp's pages: i0 + warp + kWarps k, k < mine; lane k % 32 knows page k's place in the pool and its ordinal
   const int mine = max(0, (ip - i0 - warp + kWarps - 1) / kWarps);
-  unsigned char* ring = dyn + (size_t)warp * kRing * raw_bytes(D);
-  int ord = 0;
-  long long pid = -1;
-  auto look_up = [&](int k0, int& o, long long& p) {
+  int ord = 0, pid = -1;
+  auto look_up = [&](int k0, int& o, int& p) {
     p = -1;
     if (k0 + lane < mine) {
       const int i = i0 + warp + kWarps * (k0 + lane);
-      o = it.list ? it.list[i] : i;
-      if (o >= 0 && o < np) p = C.block_table[(size_t)cb * C.max_pages + o];
+      o = list ? list[i] : i;
+      if (o >= 0 && o < it.np) p = C.block_table[(size_t)cb * C.max_pages + o];
       if (p < 0 || p >= C.n_pages) {
         atomicOr(&g_int8_decode_err, TQ_DEVERR_PAGE_INDEX);
         p = -1;
       }
     }
   };
-  auto fetch = [&](long long p, int slot) {  // one lane
+  const unsigned char* first = C.pool + (size_t)g * P.sub_bytes + i8_off_head(D);
+  const size_t stride = (size_t)P.hkv * P.sub_bytes;
+  auto fetch = [&](int p, int slot) {  // one lane
     const uint32_t bar = smem_u32(&sh.full[warp][slot]);
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(raw_bytes(D)) : "memory");
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                      smem_u32(ring + slot * raw_bytes(D))),
-                 "l"(i8_subblock(P, C, p, g) + i8_off_head(D)), "r"(raw_bytes(D)), "r"(bar)
+                 "l"(first + (size_t)p * stride), "r"(raw_bytes(D)), "r"(bar)
                  : "memory");
   };
-  if (lane == 0) {
-    for (int i = 0; i < kRing; ++i)
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&sh.full[warp][i])) : "memory");
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
   look_up(0, ord, pid);
   __syncwarp();
 #pragma unroll
   for (int k = 0; k < kRing; ++k) {
-    const long long p = __shfl_sync(0xffffffffu, pid, k);
-    if (lane == 0 && k < mine && p >= 0) fetch(p, k);
+    const int p = __shfl_sync(0xffffffffu, pid, k), sl = slot + k >= kRing ? slot + k - kRing : slot + k;
+    if (k < mine && p >= 0) {
+      if (lane == 0) fetch(p, sl);
+      fly |= 1u << sl;
+    }
   }
 
   load_query<D>(sh, q, dtype, head0, G, P.dh);
-  const float qs = sh.unscale[g8] * scale;
+  const float qs = sh.unscale[g8] * scale * kLog2e;  // scores in powers of two
 
   float acc[J][2][4][4];
 #pragma unroll
@@ -225,41 +233,39 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
         for (int r = 0; r < 4; ++r) acc[j][h][i][r] = 0.f;
   float m = -INFINITY, l = 0.f, vref = 0.f;  // of head g8 (l: this lane's tokens)
 
-  // scores -> weights in operand order; the running state and the accumulators follow
-  auto softmax = [&](const float (&sacc)[2][4], float ks, float vs, int pos0, int live_to) -> uint4 {
+  // products -> scores (times f) -> weights in operand order; the running state and the accumulators follow.
+  // Tokens pos0 .. of which those before live_to count.
+  auto softmax = [&](const float (&sacc)[2][4], float f, float vs, int pos0, int live_to) -> uint4 {
     // head g8, tokens 4 t4 + 2 nt + e
-    float x[2][2], mx = -INFINITY;
+    float x[2][2];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int pos = pos0 + 4 * t4 + 2 * nt + e;
-        const float lg = (sacc[nt][e] + sacc[nt][e + 2]) * (qs * ks);
-        x[nt][e] = pos < live_to ? lg : -INFINITY;
-        mx = fmaxf(mx, x[nt][e]);
-        if (scores && g8 < G && pos < live_to) scores[(head0 + g8) * (size_t)max_ctx + pos] = lg;
-      }
+      for (int e = 0; e < 2; ++e) x[nt][e] = (sacc[nt][e] + sacc[nt][e + 2]) * f;
+    if (pos0 + kPage > live_to || scores) {
+#pragma unroll
+      for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int pos = pos0 + 4 * t4 + 2 * nt + e;
+          if (pos >= live_to) x[nt][e] = -INFINITY;
+          else if (scores && g8 < G) scores[(head0 + g8) * (size_t)max_ctx + pos] = x[nt][e] * kLn2;
+        }
+    }
+    float mx = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const float mn = fmaxf(m, mx);
     const float vn = fmaxf(vref, pow2_above(vs));
     // a score that is NaN leaves mn as it was and makes its weights NaN
     const float mb = mn == -INFINITY ? 0.f : mn;
-    const float al = exp2f((m - mb) * kLog2e);  // 0 before the first score
-    const float av = vn > 0.f ? al * (vref * pow2_inv(vn)) : al;
-    const float wv = vn > 0.f ? vs * pow2_inv(vn) * kWeightTop : 0.f;
-    m = mn;
-    vref = vn;
-    l *= al;
-    float p[2][2];
-#pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        p[nt][e] = exp2f((x[nt][e] - mb) * kLog2e);
-        l += p[nt][e];
-      }
-    if (__any_sync(0xffffffffu, av != 1.f)) {
+    const float vi = vn > 0.f ? pow2_inv(vn) : 0.f;
+    if (__any_sync(0xffffffffu, mn != m || vn != vref)) {
+      const float al = ex2(m - mb);  // 0 before the first score
+      const float av = vn > 0.f ? al * (vref * vi) : al;
+      m = mn;
+      vref = vn;
+      l *= al;
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -269,26 +275,27 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[j][h][i4][r] *= av;
     }
+    const float wv = vs * vi * kWeightTop;
+    float p[2][2];
+#pragma unroll
+    for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        p[nt][e] = ex2(x[nt][e] - mb);
+        l += p[nt][e];
+      }
     uint4 a;
     split2(p[0][0] * wv, p[0][1] * wv, a.x, a.y);
     split2(p[1][0] * wv, p[1][1] * wv, a.z, a.w);
     return a;
   };
 
-  bool failed = false;
-  uint32_t fly = 0;  // slots with a copy in flight (this warp's next phases)
-  uint32_t phase = 0;
-  int slot = 0;
-#pragma unroll
-  for (int k = 0; k < kRing; ++k)
-    if (k < mine && __shfl_sync(0xffffffffu, pid, k) >= 0) fly |= 1u << k;
-  int nord = 0;
-  long long npid = -1;
+  int nord = 0, npid = -1;
 #pragma unroll 1
   for (int k = 0; k < mine; ++k) {
     const int k32 = k & 31;
     if (k32 == 32 - kRing) look_up((k & ~31) + 32, nord, npid);  // the next 32, before the copies ahead reach them
-    const long long p = __shfl_sync(0xffffffffu, pid, k32);
+    const int p = __shfl_sync(0xffffffffu, pid, k32);
     const int o = __shfl_sync(0xffffffffu, ord, k32);
     if (p >= 0) {
       if (!__all_sync(0xffffffffu, mbar_wait(&sh.full[warp][slot], phase >> slot & 1))) {
@@ -301,16 +308,18 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
       const float2 sc = *reinterpret_cast<const float2*>(sb);
       float sacc[2][4] = {};
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt)
+      for (int j = 0; j < J; ++j) {
+        const uint4 w0 = *reinterpret_cast<const uint4*>(sb + kI8Head + j * 512 + lane * 16);
+        const uint4 w1 = *reinterpret_cast<const uint4*>(sb + kI8Head + 8 * D + j * 512 + lane * 16);
+        const uint32_t c0[4] = {w0.x, w0.y, w0.z, w0.w}, c1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const uint4 w = *reinterpret_cast<const uint4*>(sb + kI8Head + nt * 8 * D + j * 512 + lane * 16);
-          mma16816(sacc[nt], sh.afr[4 * j][lane], i8_lo2(w.x), i8_hi2(w.x));
-          mma16816(sacc[nt], sh.afr[4 * j + 1][lane], i8_lo2(w.y), i8_hi2(w.y));
-          mma16816(sacc[nt], sh.afr[4 * j + 2][lane], i8_lo2(w.z), i8_hi2(w.z));
-          mma16816(sacc[nt], sh.afr[4 * j + 3][lane], i8_lo2(w.w), i8_hi2(w.w));
+        for (int i = 0; i < 4; ++i) {
+          const uint4 qa = sh.afr[4 * j + i][lane];
+          mma16816(sacc[0], qa, i8_lo2(c0[i]), i8_hi2(c0[i]));
+          mma16816(sacc[1], qa, i8_lo2(c1[i]), i8_hi2(c1[i]));
         }
-      const uint4 a = softmax(sacc, sc.x, sc.y, o * kPage, it.nc);
+      }
+      const uint4 a = softmax(sacc, qs * sc.x, sc.y, o * kPage, it.nc);
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -325,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
     }
     // the page kRing on takes this one's slot
     const int ka = k + kRing;
-    const long long pn = __shfl_sync(0xffffffffu, (ka ^ k) & 32 ? npid : pid, ka & 31);
+    const int pn = __shfl_sync(0xffffffffu, (ka ^ k) & 32 ? npid : pid, ka & 31);
     if (ka < mine && pn >= 0) {
       if (lane == 0) fetch(pn, slot);
       fly |= 1u << slot;
@@ -336,18 +345,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
       ord = nord;
     }
   }
-  if (failed) {
-    if (lane == 0) atomicOr(&g_int8_decode_err, TQ_DEVERR_TIMEOUT);
-    for (int i = 0; i < kRing; ++i)  // copies in flight land before the block's memory is given up
-      if (fly >> i & 1) (void)mbar_wait(&sh.full[warp][i], phase >> i & 1);
-  }
   // window groups [max(i0, pages), i1), counted on after the pages so that the warps' shares stay even
   {
     const int w0 = max(i0, it.pages);
     int i = w0 + (warp + kWarps - (w0 - i0) % kWarps) % kWarps;
 #pragma unroll 1
     for (; i < i1; i += kWarps) {
-      const int pos0 = it.nc + (i - it.pages) * kPage, live_to = it.nc + nwin;
+      const int pos0 = it.nc + (i - it.pages) * kPage, live_to = it.nc + it.nwin;
       const __half* kring = C.win_k + ((size_t)cb * P.hkv + g) * C.ring * D;
       float sacc[2][4] = {};
 #pragma unroll
@@ -367,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
           mma16816(sacc[nt], sh.afr[4 * j + 3][lane], w1.z, w1.w);
         }
       }
-      const uint4 a = softmax(sacc, 1.f, 1.f, pos0, live_to);
+      const uint4 a = softmax(sacc, qs, 1.f, pos0, live_to);
       const __half* vring = C.win_v + ((size_t)cb * P.hkv + g) * C.ring * D;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
@@ -394,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
     sh.m[warp][g8] = m;
     sh.l[warp][g8] = l;
   }
-  const float unit = vref * (1.f / kWeightTop);
+  const float undo = vref * (1.f / kWeightTop);
   float* merge = reinterpret_cast<float*>(dyn);
   __syncthreads();  // every warp's ring is idle
   float* box = merge + ((size_t)warp * 8 + g8) * D;
@@ -405,8 +409,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         *reinterpret_cast<float4*>(box + 64 * j + 16 * t4 + 8 * c + 4 * h) =
-            make_float4((acc[j][h][0][c] + acc[j][h][0][c + 2]) * unit, (acc[j][h][1][c] + acc[j][h][1][c + 2]) * unit,
-                        (acc[j][h][2][c] + acc[j][h][2][c + 2]) * unit, (acc[j][h][3][c] + acc[j][h][3][c + 2]) * unit);
+            make_float4((acc[j][h][0][c] + acc[j][h][0][c + 2]) * undo, (acc[j][h][1][c] + acc[j][h][1][c + 2]) * undo,
+                        (acc[j][h][2][c] + acc[j][h][2][c + 2]) * undo, (acc[j][h][3][c] + acc[j][h][3][c + 2]) * undo);
   __syncthreads();
   for (int i = tid; i < G * D; i += kThreads) {
     const int h = i / D, j = i % D;
@@ -417,52 +421,77 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
     float sum = 0.f, o = 0.f;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = exp2f((sh.m[w][h] - mb) * kLog2e);
+      const float f = ex2(sh.m[w][h] - mb);
       sum = fmaf(f, sh.l[w][h], sum);
       o = fmaf(f, merge[((size_t)w * 8 + h) * D + j], o);
     }
     if (S == 1) {
       // nothing visible: 0 and -inf; a NaN sum passes through
       if (j < P.dh) out[(head0 + h) * P.dh + j] = sum == 0.f ? 0.f : o / sum;
-      if (lse && j == 0) lse[head0 + h] = sum == 0.f ? -INFINITY : M + logf(sum);
+      if (lse && j == 0) lse[head0 + h] = sum == 0.f ? -INFINITY : M * kLn2 + logf(sum);
     } else {
-      reinterpret_cast<float*>(ws + L.acc)[((head0 + h) * S + s) * D + j] = o;
-      if (j == 0) {
-        float* ml = reinterpret_cast<float*>(ws + L.ml) + ((head0 + h) * S + s) * 2;
-        ml[0] = M;
-        ml[1] = sum;
-      }
+      const size_t row = (head0 + h) * S + s;
+      reinterpret_cast<float*>(ws + L.acc)[row * D + j] = o;
+      if (j == 0) reinterpret_cast<float2*>(ws + L.ml)[row] = make_float2(M, sum);
     }
+  }
+  if (failed) {
+    if (lane == 0) atomicOr(&g_int8_decode_err, TQ_DEVERR_TIMEOUT);
+    for (int i = 0; i < kRing; ++i)  // copies in flight land before the block's memory is given up
+      if (fly >> i & 1) (void)mbar_wait(&sh.full[warp][i], phase >> i & 1);
   }
 }
 
-// Joins the splits of one query head in their order; LOG2: their references are powers of two, else of e.
-template <int D, bool LOG2>
-__global__ void __launch_bounds__(D / 4) i8_combine_kernel(const unsigned char* ws, WsLayout L, int hq, int dh, float* out,
-                                                           float* lse) {
-  const int S = L.n_comp_splits, j = threadIdx.x;
-  const size_t head = (size_t)blockIdx.y * hq + blockIdx.x;
-  const float2* ml = reinterpret_cast<const float2*>(ws + L.ml) + head * S;
-  const float4* acc = reinterpret_cast<const float4*>(ws + L.acc) + head * S * (D / 4) + j;
+// Joins n partial results of one query head, row(0), row(1) .. in that order; references in powers of two.  D / 4 threads.
+template <int D, typename Row>
+__device__ __forceinline__ void join(const float2* ml, const float4* acc, int n, Row row, float* out, float* lse, int dh) {
+  const int j = threadIdx.x;
   float M = -INFINITY;
-  for (int s = 0; s < S; ++s) M = fmaxf(M, ml[s].x);
+  for (int s = 0; s < n; ++s) M = fmaxf(M, ml[row(s)].x);
   const float mb = M == -INFINITY ? 0.f : M;
   float sum = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int s = 0; s < S; ++s) {
-    const float f = exp2f((ml[s].x - mb) * (LOG2 ? 1.f : kLog2e));
-    if (ml[s].y == 0.f) continue;  // a split that saw nothing may not have written its sums
-    const float4 a = acc[(size_t)s * (D / 4)];
-    sum = fmaf(f, ml[s].y, sum);
+  for (int s = 0; s < n; ++s) {
+    const float2 p = ml[row(s)];
+    const float f = ex2(p.x - mb);
+    if (p.y == 0.f) continue;  // a split that saw nothing may not have written its sums
+    const float4 a = acc[row(s) * (D / 4) + j];
+    sum = fmaf(f, p.y, sum);
     o.x = fmaf(f, a.x, o.x);
     o.y = fmaf(f, a.y, o.y);
     o.z = fmaf(f, a.z, o.z);
     o.w = fmaf(f, a.w, o.w);
   }
   const float z = sum == 0.f ? 0.f : 1.f / sum;
-  if (4 * j < dh) *reinterpret_cast<float4*>(out + head * dh + 4 * j) = make_float4(o.x * z, o.y * z, o.z * z, o.w * z);
-  if (lse && j == 0) lse[head] = sum == 0.f ? -INFINITY : (LOG2 ? M * 0.6931471805599453f : M) + logf(sum);
+  if (4 * j < dh) *reinterpret_cast<float4*>(out + 4 * j) = make_float4(o.x * z, o.y * z, o.z * z, o.w * z);
+  if (lse && j == 0) *lse = sum == 0.f ? -INFINITY : M * kLn2 + logf(sum);
+}
+
+// Equal parts of every unit: row = head * splits + split.
+template <int D>
+__global__ void __launch_bounds__(D / 4) i8_combine_kernel(const unsigned char* ws, WsLayout L, int hq, int dh, float* out,
+                                                           float* lse) {
+  const size_t head = (size_t)blockIdx.y * hq + blockIdx.x, S = L.n_comp_splits;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  join<D>(reinterpret_cast<const float2*>(ws + L.ml), reinterpret_cast<const float4*>(ws + L.acc), L.n_comp_splits,
+          [&](int s) { return head * S + s; }, out + head * dh, lse ? lse + head : nullptr, dh);
+}
+
+// Launch as a programmatic dependent of the kernel before it in the stream.
+template <typename... K, typename... A>
+cudaError_t launch_after(void (*kern)(K...), dim3 grid, int threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<K>(args)...);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int D>
@@ -472,25 +501,28 @@ cudaError_t decode(const KParams& P, const KCache& C, const void* q, int dtype, 
   const size_t dyn = std::max((size_t)kWarps * kRing * raw_bytes(D), (size_t)kWarps * 8 * D * sizeof(float));
   cudaError_t e = cudaFuncSetAttribute(i8_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn);
   if (e != cudaSuccess) return e;
-  const dim3 grid(L.n_comp_splits, P.hkv, C.batch);
-  i8_decode_kernel<D><<<grid, kThreads, dyn, st>>>(P, C, q, dtype, scale, pages, counts, n_sel, out, lse, scores, ws, L,
-                                                   max_ctx);
+  i8_decode_kernel<D><<<dim3(L.n_comp_splits, P.hkv, C.batch), kThreads, dyn, st>>>(P, C, q, dtype, scale, pages, counts, n_sel,
+                                                                                out, lse, scores, ws, L, max_ctx);
   e = cudaGetLastError();
   if (e != cudaSuccess || L.n_comp_splits == 1) return e;
-  return launch_int8_combine(P, ws, L, C.batch, false, out, lse, st);
+  return launch_int8_combine(P, ws, L, C.batch, out, lse, st);
 }
 
 }  // namespace
 
-// At most max_items groups of 16 tokens a sequence (pages and window), split so that the grid fills the
-// SMs twice over, but a split keeps two groups for each of its warps.
+// At most max_items groups of 16 tokens a sequence (pages and window).  One wave of blocks where that gives a
+// unit four splits or more (one sequence of 262144 tokens, 8 heads: 76 splits 114 us, two waves 126 us); else two
+// waves, since few splits of unequal sequences leave a long tail (32 x 8192 tokens, 8 heads: 2 or 3 splits 103 us, 5
+// splits 93 us).  A split keeps a group for each of its warps.  (Blocks that share all sequences' groups evenly in
+// one wave were no faster, 95 us, and would make a sequence's rounding depend on the others in its batch.)
 WsLayout int8_ws_layout(const KParams& P, int batch, long long max_items, int n_splits, int num_sms) {
   WsLayout L{};
   long long S = n_splits;
   if (S <= 0) {
-    const long long units = std::max(1LL, (long long)batch * P.hkv);
-    S = (2LL * ctas_per_sm(P.d) * num_sms + units - 1) / units;
-    S = std::min(S, (max_items + 2 * kWarps - 1) / (2 * kWarps));
+    const long long units = std::max(1LL, (long long)batch * P.hkv), slots = (long long)ctas_per_sm(P.d) * num_sms;
+    S = slots / units;
+    if (S < 4) S = (2 * slots + units - 1) / units;
+    S = std::min(S, (max_items + kWarps - 1) / kWarps);
   }
   S = std::max(1LL, std::min(S, std::min(max_items, 65535LL)));
   L.n_comp_splits = (int)S;
@@ -498,7 +530,7 @@ WsLayout int8_ws_layout(const KParams& P, int batch, long long max_items, int n_
   size_t o = 0;
   if (S > 1) {
     L.ml = o;
-    o = align256(o + heads * S * 2 * sizeof(float));
+    o = align256(o + heads * S * sizeof(float2));
     L.acc = o;
     o = align256(o + heads * S * (size_t)P.d * sizeof(float));
   }
@@ -515,12 +547,10 @@ cudaError_t launch_int8_decode(const KParams& P, const KCache& C, const void* q,
   return decode<256>(P, C, q, dtype, scale, pages, counts, n_sel, out, lse, scores, w, L, max_ctx, st);
 }
 
-cudaError_t launch_int8_combine(const KParams& P, const unsigned char* ws, const WsLayout& L, long long rows, bool log2,
-                                float* out, float* lse, cudaStream_t st) {
-  const dim3 grid(P.hq, (unsigned)rows);
-  auto kern = P.d == 128 ? (log2 ? i8_combine_kernel<128, true> : i8_combine_kernel<128, false>) : i8_combine_kernel<256, false>;
-  kern<<<grid, P.d / 4, 0, st>>>(ws, L, P.hq, P.dh, out, lse);
-  return cudaGetLastError();
+cudaError_t launch_int8_combine(const KParams& P, const unsigned char* ws, const WsLayout& L, long long rows, float* out,
+                                float* lse, cudaStream_t st) {
+  auto kern = P.d == 128 ? i8_combine_kernel<128> : i8_combine_kernel<256>;
+  return launch_after(kern, dim3(P.hq, (unsigned)rows), P.d / 4, st, ws, L, P.hq, P.dh, out, lse);
 }
 
 cudaError_t read_clear_int8_decode_error(unsigned* bits) {

@@ -843,7 +843,7 @@ cudaError_t launch_int8_prefill(const KParams& P, const KCache& C, int n_query, 
   kern<<<dim3((rows + per - 1) / per, P.hkv, C.batch * L.n_comp_splits), kThreads, kSmemBytes, st>>>(P, C, n_query, q, dtype, scale,
                                                                                                  out, lse, w, K, max_ctx);
   if ((e = cudaGetLastError()) != cudaSuccess || J.n_comp_splits == 1) return e;
-  return launch_int8_combine(P, w, J, (long long)C.batch * n_query, true, out, lse, st);
+  return launch_int8_combine(P, w, J, (long long)C.batch * n_query, out, lse, st);
 }
 
 cudaError_t read_clear_int8_prefill_error(unsigned* bits) {
