@@ -122,18 +122,29 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+_torch = None  # (imported by the first call that needs it)
+_codes: dict = {}
+
+
+def _load_torch():
+    global _torch
+    import torch
+
+    _codes.update({torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16})
+    _torch = torch
+    return torch
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-
-        return torch.cuda.current_stream().cuda_stream
+        return (_torch or _load_torch()).cuda.current_stream().cuda_stream
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def dtype_code(t) -> int:
-    import torch
-
-    return {torch.float32: TQ_F32, torch.bfloat16: TQ_BF16, torch.float16: TQ_F16}[t.dtype]
+    if _torch is None:
+        _load_torch()
+    return _codes[t.dtype]
 
 
 # ---------------------------------------------------------------------------- host setup

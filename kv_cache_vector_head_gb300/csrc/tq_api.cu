@@ -503,7 +503,7 @@ extern "C" tq_status tq_select_pages(const tq_layer_params* p, const tq_cache* c
     set_error("workspace too small: %zu < %zu", workspace_bytes, select_ws_bytes(K, cache->batch, max_ctx));
     return TQ_ERR_CAPACITY;
   }
-  return cuda_status(launch_select(K, C, q, dtype, n_sel, n_sink, n_recent, pages, counts, workspace, max_ctx,
+  return cuda_status(launch_select(K, C, q, dtype, n_sel, n_sink, n_recent, pages, counts, workspace, max_ctx, num_sms(),
                                    reinterpret_cast<cudaStream_t>(stream)),
                      "tq_select_pages");
 }

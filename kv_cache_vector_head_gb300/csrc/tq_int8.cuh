@@ -64,6 +64,22 @@ __device__ __forceinline__ uint32_t i8_code(float x, float s, float inv) {
   return bits;
 }
 
+// Codes + 128 of two values in the low bytes of lo, hi; the larger residual goes into rm: where that reaches half a
+// step at the end, a value was not finite or lay on a half step, and i8_code() decides.
+__device__ __forceinline__ void i8_code2(float x, float y, uint64_t inv2, uint64_t ns2, uint32_t& lo, uint32_t& hi, float& rm) {
+  // 1.5 2^23 + 128: the rounded sum's low byte is code + 128
+  constexpr uint64_t kMagic2 = 0x4B4000804B400080ull, kMinus2 = 0xCB400080CB400080ull;
+  uint64_t v, m, c, r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(m) : "l"(v), "l"(inv2), "l"(kMagic2));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(c) : "l"(m), "l"(kMinus2));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(c), "l"(ns2), "l"(v));
+  float r0, r1;
+  asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(m));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r0), "=f"(r1) : "l"(r));
+  rm = fmaxf(rm, fmaxf(fabsf(r0), fabsf(r1)));
+}
+
 // Low bytes of four words as one word.
 __device__ __forceinline__ uint32_t i8_pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   uint32_t lo, hi, r;

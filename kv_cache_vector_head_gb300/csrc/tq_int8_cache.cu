@@ -6,7 +6,10 @@
 // 512 contiguous.  Every element is read once and no shared memory is used; what bounds the kernel is
 // the traffic (2 or 4 bytes in and 1 out an element).
 #include <algorithm>
+#include <map>
+#include <mutex>
 #include <type_traits>
+#include <utility>
 
 #include "tq_int8.cuh"
 #include "tq_launch.h"
@@ -19,120 +22,162 @@ namespace {
 
 constexpr int kWriteWarps = 4;
 
-// Byte-wise signed minimum / maximum over the lanes with the same t4 (lane bits 2..4).
-__device__ __forceinline__ uint32_t min_over_g8(uint32_t v) {
-#pragma unroll
-  for (int o = 4; o < 32; o <<= 1) v = __vmins4(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
-__device__ __forceinline__ uint32_t max_over_g8(uint32_t v) {
-#pragma unroll
-  for (int o = 4; o < 32; o <<= 1) v = __vmaxs4(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+__device__ __forceinline__ uint32_t min_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("min.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Bits of the largest magnitude in a lane's pieces: finite values order as their bits do, what is not finite is above
+// them all.  (16-bit types two at a time.)
+template <typename T>
+__device__ __forceinline__ uint32_t top_bits(uint32_t top, const uint4& w) {
+  if constexpr (sizeof(T) == 4) {
+    top = max(top, max(max(w.x & 0x7fffffffu, w.y & 0x7fffffffu), max(w.z & 0x7fffffffu, w.w & 0x7fffffffu)));
+  } else {
+    top = max_u16x2(top, max_u16x2(max_u16x2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), max_u16x2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+  }
+  return top;
+}
+// The warp's largest magnitude from its lanes' bits; finite: there is nothing that is not.
+template <typename T>
+__device__ __forceinline__ float top_of(uint32_t top, bool& finite) {
+  if constexpr (sizeof(T) == 4) {
+    top = __reduce_max_sync(0xffffffffu, top);
+    finite = top <= 0x7f7fffffu;
+    return __uint_as_float(top);
+  } else {
+    top = __reduce_max_sync(0xffffffffu, max(top & 0xffffu, top >> 16));
+    if constexpr (std::is_same<T, __half>::value) {
+      finite = top <= 0x7bffu;
+      return __half2float(__ushort_as_half((unsigned short)top));
+    } else {
+      finite = top <= 0x7f7fu;
+      return __uint_as_float(top << 16);
+    }
+  }
 }
 
 // Quantizes 16 tokens of one head into sub-block sb; row(t) is token t's row of dh elements of type T
-// (16-byte aligned), dims dh .. D-1 are zero.
+// (16-byte aligned), dims dh .. D-1 are zero.  An element costs two packed fused multiply-adds and an addition; a page with
+// an exact half step or with something that is not finite is gone over once more, element by element.
 template <int D, typename T, typename Row>
 __device__ __forceinline__ void i8_write_page(Row row, int dh, bool is_key, unsigned char* sb) {
   constexpr int EPL = 16 / (int)sizeof(T);  // elements of a 16-byte load
   constexpr int J = D / 64;
+  constexpr int L = 16 / EPL;  // loads of 16 elements: 16 dims of a token (keys), 8 dims of two tokens (values)
   const int lane = threadIdx.x & 31, g8 = lane >> 2, t4 = lane & 3;
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  if (is_key) {
-    constexpr int L = 16 / EPL;
-    uint4 raw[2][J][L];
-    float a = 0.f;
+  // keys: [j][nt] 16 dims 64 j + 16 t4 .. of token 4 (g8 / 2) + 2 nt + g8 % 2
+  // values: [j][pair] 8 dims 64 j + 8 g8 .. of tokens 4 t4 + 2 pair, + 1
+  uint4 raw[J][2][L];
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt) {
-      const T* r = row(4 * (g8 >> 1) + 2 * nt + (g8 & 1));
+  for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int j = 0; j < J; ++j)
+    for (int l = 0; l < L; ++l) {
+      const int tok = is_key ? 4 * (g8 >> 1) + 2 * h + (g8 & 1) : 4 * t4 + 2 * h + l / (L / 2);
+      const int c0 = is_key ? 16 * t4 + l * EPL : 8 * g8 + l % (L / 2) * EPL;
+      const T* r = row(tok);
 #pragma unroll
-        for (int l = 0; l < L; ++l) {
-          const int c = 64 * j + 16 * t4 + l * EPL;  // dh is a multiple of 8, so a piece is in or out
-          raw[nt][j][l] = c < dh ? *reinterpret_cast<const uint4*>(r + c) : zero;
-        }
+      for (int j = 0; j < J; ++j)  // dh is a multiple of 8, so a piece is in or out
+        raw[j][h][l] = 64 * j + c0 < dh ? *reinterpret_cast<const uint4*>(r + 64 * j + c0) : zero;
     }
+  uint32_t top = 0;
 #pragma unroll
-    for (int nt = 0; nt < 2; ++nt)
+  for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int j = 0; j < J; ++j)
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int l = 0; l < L; ++l) top = top_bits<T>(top, raw[j][h][l]);
+  bool finite;
+  float a = top_of<T>(top, finite);
+  if (!finite) {
+    a = 0.f;
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int l = 0; l < L; ++l)
 #pragma unroll
-          for (int e = 0; e < EPL; ++e) a = fmaxf(a, i8_mag(elem_of<T>(raw[nt][j][l], e)));
-    const float s = i8_scale(warp_max_f(a)), inv = s > 0.f ? __frcp_rn(s) : 0.f;
+          for (int e = 0; e < EPL; ++e) a = fmaxf(a, i8_mag(elem_of<T>(raw[j][h][l], e)));
+    a = warp_max_f(a);
+  }
+  const float s = i8_scale(a), inv = s > 0.f ? __frcp_rn(s) : 0.f;
+  uint64_t inv2, ns2;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(inv2) : "f"(inv));
+  asm("mov.b64 %0, {%1, %1};" : "=l"(ns2) : "f"(-s));
+  float rm = 0.f;
+  // element e of 16 in raw[j][h]
+  auto x = [&](int j, int h, int e) { return elem_of<T>(raw[j][h][e / EPL], e % EPL); };
+  auto codes = [&](bool slow) {
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-      uint32_t mn[4], mx[4];
+      uint32_t u[2][16];
 #pragma unroll
-      for (int nt = 0; nt < 2; ++nt) {
-        uint32_t w[4];
+      for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t u[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            u[e] = i8_code(elem_of<T>(raw[nt][j][(4 * i + e) / EPL], (4 * i + e) % EPL), s, inv);
-          w[i] = i8_pack4(u[0], u[1], u[2], u[3]);
-          const uint32_t sc = w[i] ^ 0x80808080u;  // signed codes
-          mn[i] = nt == 0 ? sc : __vmins4(mn[i], sc);
-          mx[i] = nt == 0 ? sc : __vmaxs4(mx[i], sc);
+        for (int e = 0; e < 16; e += 2) {
+          if (slow) {
+            u[h][e] = i8_code(x(j, h, e), s, inv);
+            u[h][e + 1] = i8_code(x(j, h, e + 1), s, inv);
+          } else {
+            i8_code2(x(j, h, e), x(j, h, e + 1), inv2, ns2, u[h][e], u[h][e + 1], rm);
+          }
         }
-        *reinterpret_cast<uint4*>(sb + i8_off_kcodes(D) + nt * 8 * D + j * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      if (is_key) {
+        uint32_t mn[8], mx[8];  // channels 2 e, 2 e + 1 as 16-bit pairs
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        mn[i] = min_over_g8(mn[i]);
-        mx[i] = max_over_g8(mx[i]);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            w[i] = i8_pack4(u[h][4 * i], u[h][4 * i + 1], u[h][4 * i + 2], u[h][4 * i + 3]);
+            const uint32_t p = __byte_perm(w[i], 0u, 0x4140), r = __byte_perm(w[i], 0u, 0x4342);
+            mn[2 * i] = h ? min_u16x2(mn[2 * i], p) : p;
+            mn[2 * i + 1] = h ? min_u16x2(mn[2 * i + 1], r) : r;
+            mx[2 * i] = h ? max_u16x2(mx[2 * i], p) : p;
+            mx[2 * i + 1] = h ? max_u16x2(mx[2 * i + 1], r) : r;
+          }
+          *reinterpret_cast<uint4*>(sb + i8_off_kcodes(D) + h * 8 * D + j * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        // over the lanes with the same t4, halving what each carries: lane g8 ends with channels 2 g8, 2 g8 + 1
+#pragma unroll
+        for (int n = 4; n >= 1; n >>= 1) {
+          const int o = 4 * n;
+          const bool up = lane & o;
+#pragma unroll
+          for (int i = 0; i < n; ++i) {
+            const uint32_t gm = __shfl_xor_sync(0xffffffffu, up ? mn[i] : mn[n + i], o);
+            const uint32_t gx = __shfl_xor_sync(0xffffffffu, up ? mx[i] : mx[n + i], o);
+            mn[i] = min_u16x2(up ? mn[n + i] : mn[i], gm);
+            mx[i] = max_u16x2(up ? mx[n + i] : mx[i], gx);
+          }
+        }
+        const int at = 64 * j + 16 * t4 + 2 * g8;
+        *reinterpret_cast<unsigned short*>(sb + at) = (unsigned short)(__byte_perm(mn[0], 0u, 0x4420) ^ 0x8080u);
+        *reinterpret_cast<unsigned short*>(sb + D + at) = (unsigned short)(__byte_perm(mx[0], 0u, 0x4420) ^ 0x8080u);
+      } else {
+        // u[h][8 t + d]: token 4 t4 + 2 h + t, dim d of 8
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = i8_pack4(u[0][4 * half + i], u[0][8 + 4 * half + i], u[1][4 * half + i], u[1][8 + 4 * half + i]);
+          *reinterpret_cast<uint4*>(sb + i8_off_vcodes(D) + j * 1024 + half * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
       }
-      if (g8 == 0) *reinterpret_cast<uint4*>(sb + 64 * j + 16 * t4) = make_uint4(mn[0], mn[1], mn[2], mn[3]);
-      if (g8 == 1) *reinterpret_cast<uint4*>(sb + D + 64 * j + 16 * t4) = make_uint4(mx[0], mx[1], mx[2], mx[3]);
     }
-    if (lane == 0) *reinterpret_cast<float*>(sb + i8_off_head(D)) = s;
-    if (lane >= 2 && lane < 8) *reinterpret_cast<float*>(sb + i8_off_head(D) + 4 * lane) = 0.f;  // the padding
-  } else {
-    constexpr int L = 8 / EPL;
-    uint4 raw[J][4][L];
-    float a = 0.f;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const T* r = row(4 * t4 + t);
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-#pragma unroll
-        for (int l = 0; l < L; ++l) {
-          const int c = 64 * j + 8 * g8 + l * EPL;
-          raw[j][t][l] = c < dh ? *reinterpret_cast<const uint4*>(r + c) : zero;
-        }
-    }
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int l = 0; l < L; ++l)
-#pragma unroll
-          for (int e = 0; e < EPL; ++e) a = fmaxf(a, i8_mag(elem_of<T>(raw[j][t][l], e)));
-    const float s = i8_scale(warp_max_f(a)), inv = s > 0.f ? __frcp_rn(s) : 0.f;
-#pragma unroll
-    for (int j = 0; j < J; ++j)
-#pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t u[4];
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-            u[t] = i8_code(elem_of<T>(raw[j][t][(4 * half + i) / EPL], (4 * half + i) % EPL), s, inv);
-          w[i] = i8_pack4(u[0], u[1], u[2], u[3]);
-        }
-        *reinterpret_cast<uint4*>(sb + i8_off_vcodes(D) + j * 1024 + half * 512 + lane * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    if (lane == 0) *reinterpret_cast<float*>(sb + i8_off_head(D) + 4) = s;
-  }
+  };
+  codes(false);
+  if (__any_sync(0xffffffffu, !finite || (s > 0.f && !(rm < 0.5f * s)))) codes(true);
+  if (lane == 0) *reinterpret_cast<float*>(sb + i8_off_head(D) + (is_key ? 0 : 4)) = s;
+  if (is_key && lane >= 2 && lane < 8) *reinterpret_cast<float*>(sb + i8_off_head(D) + 4 * lane) = 0.f;  // the padding
 }
 
 // One row into the float16 ring (zero tail past dh), one warp.
@@ -426,6 +471,21 @@ cudaError_t launch_int8_step(const KParams& P, const KCache& C, const void* k, c
 cudaError_t launch_int8_read(const KParams& P, const KCache& C, void* k, void* v, int dtype, int first, int n_tok,
                              cudaStream_t st) {
   return TQ_I8_DISPATCH(read, P, C, k, v, first, n_tok, st);
+}
+
+cudaError_t allow_dynamic_smem(const void* kern, size_t bytes) {
+  // (the runtime call takes about a microsecond, as much as the rest of a small call's host work)
+  static std::mutex mu;
+  static std::map<std::pair<const void*, int>, size_t> given;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lk(mu);
+  size_t& have = given[{kern, dev}];
+  if (bytes <= have || bytes <= 40 * 1024) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) have = bytes;
+  return e;
 }
 
 cudaError_t read_clear_int8_error(unsigned* bits) {

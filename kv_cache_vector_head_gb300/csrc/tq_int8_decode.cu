@@ -91,35 +91,42 @@ struct Shared {
 };
 
 // Row scale (a power of two that brings the largest magnitude into [2^13, 2^14)) and operand fragments of
-// the G query rows at q [G][dh].  All threads; ends with a barrier.
+// the G query rows at q [G][dh]: a warp holds two rows in registers, four channels a lane (eight at d = 256), so that
+// the loads of all rows are in flight at once.  All threads; ends with a barrier.
 template <int D>
 __device__ void load_query(Shared<D>& sh, const void* q, int dtype, size_t row0, int G, int dh) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int h = warp; h < 8; h += kWarps) {
+  constexpr int Q = D / 128, R = 8 / kWarps;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float x[R][Q][4];
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+      const int h = warp + kWarps * r, c = 128 * i + 4 * lane;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[r][i][e] = h < G && c < dh ? load_elem(q, dtype, (long long)((row0 + h) * dh + c + e)) : 0.f;
+    }
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int h = warp + kWarps * r;
     float a = 0.f;
-    if (h < G)
-      for (int j = lane; j < dh; j += 32) a = fmaxf(a, i8_mag(load_elem(q, dtype, (long long)((row0 + h) * dh + j))));
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a = fmaxf(a, i8_mag(x[r][i][e]));
     a = warp_max_f(a);
     // 2^(13 - floor(log2 a)); the exponent is kept where both it and its reciprocal are normal
-    const int e = a > 0.f ? min(max(140 - (int)(__float_as_uint(a) >> 23), -113), 126) : 0;
-    const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-    if (lane == 0) {
-      sh.unscale[h] = __uint_as_float((uint32_t)(127 - e) << 23);
-      sh.m[0][h] = up;
-    }
-  }
-  __syncthreads();
-  for (int i = tid; i < D / 16 * 32; i += kThreads) {
-    const int kk = i >> 5, ln = i & 31, h = ln >> 2, c = 64 * (kk >> 2) + 16 * (ln & 3) + 4 * (kk & 3);
-    uint4 f = make_uint4(0, 0, 0, 0);
-    if (h < G && c < dh) {
-      float x[4];
+    const int ex = a > 0.f ? min(max(140 - (int)(__float_as_uint(a) >> 23), -113), 126) : 0;
+    const float up = __uint_as_float((uint32_t)(127 + ex) << 23);
+    if (lane == 0) sh.unscale[h] = __uint_as_float((uint32_t)(127 - ex) << 23);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = load_elem(q, dtype, (long long)((row0 + h) * dh + c + e)) * sh.m[0][h];
-      split2(x[0], x[1], f.x, f.y);
-      split2(x[2], x[3], f.z, f.w);
+    for (int i = 0; i < Q; ++i) {
+      const int c = 128 * i + 4 * lane;
+      uint4 f;
+      split2(x[r][i][0] * up, x[r][i][1] * up, f.x, f.y);
+      split2(x[r][i][2] * up, x[r][i][3] * up, f.z, f.w);
+      sh.afr[4 * (c / 64) + c % 16 / 4][4 * h + c % 64 / 16] = f;
     }
-    sh.afr[kk][ln] = f;
   }
   __syncthreads();
 }
@@ -499,7 +506,7 @@ cudaError_t decode(const KParams& P, const KCache& C, const void* q, int dtype, 
                    const int32_t* counts, int n_sel, float* out, float* lse, float* scores, unsigned char* ws,
                    const WsLayout& L, int max_ctx, cudaStream_t st) {
   const size_t dyn = std::max((size_t)kWarps * kRing * raw_bytes(D), (size_t)kWarps * 8 * D * sizeof(float));
-  cudaError_t e = cudaFuncSetAttribute(i8_decode_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)dyn);
+  cudaError_t e = allow_dynamic_smem((const void*)i8_decode_kernel<D>, dyn);
   if (e != cudaSuccess) return e;
   i8_decode_kernel<D><<<dim3(L.n_comp_splits, P.hkv, C.batch), kThreads, dyn, st>>>(P, C, q, dtype, scale, pages, counts, n_sel,
                                                                                 out, lse, scores, ws, L, max_ctx);

@@ -833,7 +833,7 @@ cudaError_t launch_int8_prefill(const KParams& P, const KCache& C, int n_query, 
   // float queries take two limbs; a single tile of rows is split over the units by key tiles instead
   const bool one = dtype == TQ_F32 || rows <= 128;
   auto kern = dtype == TQ_F32 ? i8_prefill_attn_kernel<1, 2> : rows <= 128 ? i8_prefill_attn_kernel<1, 1> : i8_prefill_attn_kernel<2, 1>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  cudaError_t e = allow_dynamic_smem((const void*)kern, kSmemBytes);
   if (e != cudaSuccess) return e;
   const int per = one ? 128 : 256;
   WsLayout K{}, J;

@@ -9,6 +9,9 @@
 
 namespace tq {
 
+// Allows a kernel `bytes` of dynamic shared memory, once per kernel, device and size seen to be larger.
+cudaError_t allow_dynamic_smem(const void* kern, size_t bytes);
+
 cudaError_t launch_quantize_flat(const KParams& P, const void* x, int dtype, long long n_vec, bool is_key,
                                  uint32_t* codes, uint32_t* signs, float* norms, float* rnorms, cudaStream_t st);
 cudaError_t launch_append_direct(const KParams& P, const KCache& C, const void* k, const void* v, int dtype,
@@ -75,7 +78,7 @@ cudaError_t launch_int8_prefill(const KParams& P, const KCache& C, int n_query, 
 // Page selection, attention totals and eviction.
 size_t select_ws_bytes(const KParams& P, int batch, int max_ctx);
 cudaError_t launch_select(const KParams& P, const KCache& C, const void* q, int dtype, int k, int n_sink, int n_recent,
-                          int32_t* pages, int32_t* counts, void* ws, int max_ctx, cudaStream_t st);
+                          int32_t* pages, int32_t* counts, void* ws, int max_ctx, int num_sms, cudaStream_t st);
 cudaError_t launch_track(const KParams& P, const KCache& C, const float* scores, const float* lse, float* mass, int max_ctx,
                          cudaStream_t st);
 int evict_ring_limit();  // longest ring that is moved in place

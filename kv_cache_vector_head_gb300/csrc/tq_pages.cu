@@ -130,17 +130,20 @@ __device__ void pick(PickShared& sh, uint32_t* cache, int n, int keep, int n_sin
 
 // ------------------------------------------------------------------ select
 
-constexpr int kScoreThreads = 256;
-constexpr int kScorePages = 4;  // pages a thread carries: a query word read from shared memory serves four products
+constexpr int kScoreThreads = 128;
+constexpr int kScorePages = 4;   // pages a thread carries: a query word read from shared memory serves four products
 
-// order keys of the page scores, grid (page blocks, hkv, batch).  D / 16 lanes share a page, 16 channels each.
+// order keys of the page scores, grid (page blocks, hkv, batch).  D / 16 lanes share a page, 16 channels each.  What
+// bounds it is the traffic, 2 d + 4 bytes a page and head in pieces of 2 d: a block asks for its first bounds before
+// it looks at the query, and for each round's (`rounds` of them) while the one before is multiplied.
 template <int D>
 __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_constant__ KParams P,
                                                                    const __grid_constant__ KCache C, const void* q,
-                                                                   int dtype, int k, uint32_t* keys, int np_max, int max_ctx) {
-  constexpr int LP = D / 16;                   // lanes a page
-  constexpr int PB = kScoreThreads / LP * kScorePages;  // pages a block
-  __shared__ uint4 qpos[8][LP], qneg[8][LP];   // codes of the positive and of the negative queries
+                                                                   int dtype, int k, uint32_t* keys, int np_max, int max_ctx,
+                                                                   int rounds) {
+  constexpr int LP = D / 16;                                // lanes a page
+  constexpr int PR = kScoreThreads / LP * kScorePages;      // pages a round
+  __shared__ uint4 qpos[8][LP], qneg[8][LP];                // codes of the positive and of the negative queries
   __shared__ float wmax[kScoreThreads / 32];
   const int g = blockIdx.y, b = blockIdx.z, tid = threadIdx.x, lane = tid & 31, G = P.G;
   const int n = C.seq_len[b], nc = C.n_compressed[b];
@@ -148,73 +151,119 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const __grid_
     if (tid == 0 && blockIdx.x == 0 && g == 0) atomicOr(&g_pages_err, TQ_DEVERR_SEQ_LEN);
     return;
   }
-  const int np = nc / kPage, p0 = blockIdx.x * PB;
+  const int np = nc / kPage, p0 = blockIdx.x * (PR * rounds), pend = min(np, p0 + PR * rounds);
   if (np <= k || p0 >= np) return;  // every page is taken, or none is here
-  // one scale for the group's queries
-  const size_t row0 = (size_t)b * P.hq + (size_t)g * G;
-  float a = 0.f;
-  for (int i = tid; i < G * P.dh; i += kScoreThreads) a = fmaxf(a, i8_mag(load_elem(q, dtype, (long long)(row0 * P.dh + i))));
-  a = warp_max_f(a);
-  if (lane == 0) wmax[tid >> 5] = a;
-  __syncthreads();
-  a = wmax[0];
-#pragma unroll
-  for (int w = 1; w < kScoreThreads / 32; ++w) a = fmaxf(a, wmax[w]);
-  const float s = i8_scale(a), inv = s > 0.f ? __frcp_rn(s) : 0.f;
-  for (int i = tid; i < G * D; i += kScoreThreads) {
-    const int h = i / D, j = i % D;
-    const float x = j < P.dh ? load_elem(q, dtype, (long long)((row0 + h) * P.dh + j)) : 0.f;
-    const int c = (int)(i8_code(x, s, inv) & 255u) - 128;
-    reinterpret_cast<int8_t*>(&qpos[h][0])[j] = (int8_t)max(c, 0);
-    reinterpret_cast<int8_t*>(&qneg[h][0])[j] = (int8_t)min(c, 0);
-  }
-  __syncthreads();
   const int l = tid % LP, slot = tid / LP;
-  uint4 lo[kScorePages], hi[kScorePages];
-  float ks[kScorePages];
-  int pg[kScorePages];
-#pragma unroll
-  for (int u = 0; u < kScorePages; ++u) {
-    pg[u] = p0 + u * (kScoreThreads / LP) + slot;
-    lo[u] = hi[u] = make_uint4(0, 0, 0, 0);
-    ks[u] = 0.f;
-    if (pg[u] < np) {
-      const long long page = C.block_table[(size_t)b * C.max_pages + pg[u]];
+  struct Bounds {
+    uint4 lo, hi;
+    float ks;
+  };
+  // pages first + u * (threads / LP) + slot of a round
+  auto page_at = [&](int first, int u) { return first + u * (kScoreThreads / LP) + slot; };
+  auto entry = [&](int pg) { return pg < pend ? C.block_table[(size_t)b * C.max_pages + pg] : -1; };
+  auto load = [&](int pg, int page) -> Bounds {
+    Bounds x{make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0), 0.f};
+    if (pg < pend) {
       if (page < 0 || page >= C.n_pages) {
         if (l == 0) atomicOr(&g_pages_err, TQ_DEVERR_PAGE_INDEX);
       } else {
         const unsigned char* sb = i8_subblock(P, C, page, g);
-        lo[u] = *reinterpret_cast<const uint4*>(sb + 16 * l);
-        hi[u] = *reinterpret_cast<const uint4*>(sb + D + 16 * l);
-        ks[u] = *reinterpret_cast<const float*>(sb + i8_off_head(D));
+        x.lo = *reinterpret_cast<const uint4*>(sb + 16 * l);
+        x.hi = *reinterpret_cast<const uint4*>(sb + D + 16 * l);
+        x.ks = *reinterpret_cast<const float*>(sb + i8_off_head(D));
       }
     }
-  }
-  int best[kScorePages];
+    return x;
+  };
+  Bounds cur[kScorePages];
+  int next[kScorePages];
 #pragma unroll
-  for (int u = 0; u < kScorePages; ++u) best[u] = INT32_MIN;
-  for (int h = 0; h < G; ++h) {
-    const uint4 qp = qpos[h][l], qn = qneg[h][l];
+  for (int u = 0; u < kScorePages; ++u) next[u] = entry(page_at(p0, u));
 #pragma unroll
-    for (int u = 0; u < kScorePages; ++u) {
-      int v = __dp4a((int)qp.x, (int)hi[u].x, 0);
-      v = __dp4a((int)qp.y, (int)hi[u].y, v);
-      v = __dp4a((int)qp.z, (int)hi[u].z, v);
-      v = __dp4a((int)qp.w, (int)hi[u].w, v);
-      v = __dp4a((int)qn.x, (int)lo[u].x, v);
-      v = __dp4a((int)qn.y, (int)lo[u].y, v);
-      v = __dp4a((int)qn.z, (int)lo[u].z, v);
-      v = __dp4a((int)qn.w, (int)lo[u].w, v);
+  for (int u = 0; u < kScorePages; ++u) cur[u] = load(page_at(p0, u), next[u]);
 #pragma unroll
-      for (int o = 1; o < LP; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      best[u] = max(best[u], v);
+  for (int u = 0; u < kScorePages; ++u) next[u] = entry(page_at(p0 + PR, u));
+  // one scale for the group's queries; a warp holds two rows in registers, four channels a lane (eight at d = 256)
+  constexpr int Q = D / 128, W = kScoreThreads / 32, R = 8 / W;
+  const size_t row0 = (size_t)b * P.hq + (size_t)g * G;
+  const int warp = tid >> 5;
+  float x[R][Q][4], a = 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+      const int h = warp + W * r, c = 128 * i + 4 * lane;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        x[r][i][e] = h < G && c < P.dh ? load_elem(q, dtype, (long long)((row0 + h) * P.dh + c + e)) : 0.f;
     }
-  }
-  if (l == 0) {
-    uint32_t* row = keys + ((size_t)b * P.hkv + g) * np_max;
 #pragma unroll
-    for (int u = 0; u < kScorePages; ++u)
-      if (pg[u] < np) row[pg[u]] = order_key(__fmul_rn((float)best[u], ks[u]));
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < Q; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a = fmaxf(a, i8_mag(x[r][i][e]));
+  a = warp_max_f(a);
+  if (lane == 0) wmax[warp] = a;
+  __syncthreads();
+  a = wmax[0];
+#pragma unroll
+  for (int w = 1; w < W; ++w) a = fmaxf(a, wmax[w]);
+  const float s = i8_scale(a), inv = s > 0.f ? __frcp_rn(s) : 0.f;
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+      int pos[4], neg[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = (int)(i8_code(x[r][i][e], s, inv) & 255u) - 128;
+        pos[e] = max(c, 0);
+        neg[e] = min(c, 0);
+      }
+      const int word = 32 * i + lane;
+      reinterpret_cast<uint32_t*>(&qpos[warp + W * r][0])[word] = i8_pack4(pos[0], pos[1], pos[2], pos[3]);
+      reinterpret_cast<uint32_t*>(&qneg[warp + W * r][0])[word] = i8_pack4(neg[0], neg[1], neg[2], neg[3]);
+    }
+  __syncthreads();
+  uint32_t* row = keys + ((size_t)b * P.hkv + g) * np_max;
+#pragma unroll 1
+  for (int first = p0; first < pend; first += PR) {
+    Bounds ahead[kScorePages];
+#pragma unroll
+    for (int u = 0; u < kScorePages; ++u) ahead[u] = load(page_at(first + PR, u), next[u]);
+#pragma unroll
+    for (int u = 0; u < kScorePages; ++u) next[u] = entry(page_at(first + 2 * PR, u));
+    // lane l ends up with the sums of page l % 4
+    int best = INT32_MIN;
+    for (int h = 0; h < G; ++h) {
+      const uint4 qp = qpos[h][l], qn = qneg[h][l];
+      int v[kScorePages];
+#pragma unroll
+      for (int u = 0; u < kScorePages; ++u) {
+        v[u] = __dp4a((int)qp.x, (int)cur[u].hi.x, 0);
+        v[u] = __dp4a((int)qp.y, (int)cur[u].hi.y, v[u]);
+        v[u] = __dp4a((int)qp.z, (int)cur[u].hi.z, v[u]);
+        v[u] = __dp4a((int)qp.w, (int)cur[u].hi.w, v[u]);
+        v[u] = __dp4a((int)qn.x, (int)cur[u].lo.x, v[u]);
+        v[u] = __dp4a((int)qn.y, (int)cur[u].lo.y, v[u]);
+        v[u] = __dp4a((int)qn.z, (int)cur[u].lo.z, v[u]);
+        v[u] = __dp4a((int)qn.w, (int)cur[u].lo.w, v[u]);
+      }
+      // each pair of lanes keeps two pages, each four lanes one, then the sums go around
+      const int x0 = l & 1 ? v[0] : v[1], x2 = l & 1 ? v[2] : v[3];
+      const int k0 = (l & 1 ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, x0, 1);
+      const int k2 = (l & 1 ? v[3] : v[2]) + __shfl_xor_sync(0xffffffffu, x2, 1);
+      int w = (l & 2 ? k2 : k0) + __shfl_xor_sync(0xffffffffu, l & 2 ? k0 : k2, 2);
+#pragma unroll
+      for (int o = 4; o < LP; o <<= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+      best = max(best, w);
+    }
+    const float ks = l == 0 ? cur[0].ks : l == 1 ? cur[1].ks : l == 2 ? cur[2].ks : cur[3].ks;
+    const int pg = page_at(first, l & 3);
+    if (l < 4 && pg < pend) row[pg] = order_key(__fmul_rn((float)best, ks));
+#pragma unroll
+    for (int u = 0; u < kScorePages; ++u) cur[u] = ahead[u];
   }
 }
 
@@ -228,6 +277,7 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const __grid_co
   const size_t row = (size_t)b * hkv + g;
   const int n = C.seq_len[b], nc = C.n_compressed[b];
   int np = nc / kPage;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // for the keys, and for readers of the lists before the score kernel
   if (n < 0 || n > max_ctx || nc < 0 || nc > n || np > C.max_pages) np = 0;  // (flagged by the score kernel)
   int32_t* list = pages + row * k;
   const int taken = min(np, k);
@@ -306,18 +356,18 @@ __device__ __forceinline__ int dropped(const KCache& C, int b, int budget) {
 }
 
 // Window rows move with their positions: p becomes p - 16 e, so ring slot i takes slot (i + 16 e) mod ring.
-// grid (column slices, 2 hkv, batch); in place through shared memory, else straight across.
-__global__ void __launch_bounds__(256) evict_window_kernel(const __grid_constant__ KCache A, const __grid_constant__ KCache B,
-                                                           int hkv, int d, int budget, int cols) {
-  extern __shared__ uint4 buf[];  // [ring][cols / 8]
-  const int b = blockIdx.z, head = blockIdx.y >> 1, ring = A.ring;
-  const bool is_key = (blockIdx.y & 1) == 0;
+// One (sequence, head, keys or values) and `cols` of its columns from c0 on; in place through shared memory, else
+// straight across.
+__device__ void move_window(const KCache& A, const KCache& B, int hkv, int d, int budget, int cols, int c0, int hv, int b,
+                            uint4* buf) {  // [ring][cols / 8]
+  const int head = hv >> 1, ring = A.ring;
+  const bool is_key = (hv & 1) == 0;
   const size_t base = ((size_t)b * hkv + head) * ring * d;
   const __half* src = (is_key ? A.win_k : A.win_v) + base;
   __half* dst = (is_key ? B.win_k : B.win_v) + base;
   const int e = max(0, dropped(A, b, budget));
   const int by = (int)((long long)e * kPage % ring);
-  const int c0 = blockIdx.x * cols, cu = min(cols, d - c0) / 8, total = ring * cu;
+  const int cu = min(cols, d - c0) / 8, total = ring * cu;
   const bool here = src == dst;
   if (here && by == 0) return;
   for (int i = threadIdx.x; i < total; i += blockDim.x) {
@@ -334,15 +384,27 @@ __global__ void __launch_bounds__(256) evict_window_kernel(const __grid_constant
     *reinterpret_cast<uint4*>(dst + (size_t)(i / cu) * d + c0 + 8 * (i % cu)) = buf[i];
 }
 
-// One block a sequence: block table (kept pages in order, a partly filled page, the dropped pages, the rest), masses,
-// counters.  New rows are put together in the workspace first, as the outputs may be the inputs.
+// grid (column slices, 2 hkv, batch)
+__global__ void __launch_bounds__(256) evict_window_kernel(const __grid_constant__ KCache A, const __grid_constant__ KCache B,
+                                                           int hkv, int d, int budget, int cols) {
+  extern __shared__ uint4 buf[];
+  move_window(A, B, hkv, d, budget, cols, blockIdx.x * cols, blockIdx.y, blockIdx.z, buf);
+}
+
+// Blocks x = 0, one a sequence: block table (kept pages in order, a partly filled page, the dropped pages, the rest),
+// masses, counters.  New rows are put together in the workspace first, as the outputs may be the inputs.  Where they
+// are not, blocks x > 0 move the windows in the same launch.
 __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_constant__ KCache A,
                                                                   const __grid_constant__ KCache B, const float* mass,
                                                                   float* mass_out, int budget, int n_sink, int n_recent,
-                                                                  int32_t* kept, int32_t* ws) {
+                                                                  int32_t* kept, int32_t* ws, int hkv, int d) {
   extern __shared__ uint32_t cache[];
   __shared__ PickShared sh;
-  const int b = blockIdx.x, mp = A.max_pages;
+  const int b = blockIdx.y, mp = A.max_pages;
+  if (blockIdx.x > 0) {
+    move_window(A, B, hkv, d, budget, d, 0, blockIdx.x - 1, b, nullptr);
+    return;
+  }
   const int n = A.seq_len[b], nc = A.n_compressed[b], e = dropped(A, b, budget);
   const int32_t* table = A.block_table + (size_t)b * mp;
   int32_t* table_out = const_cast<int32_t*>(B.block_table) + (size_t)b * mp;
@@ -400,12 +462,6 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
 
 size_t key_cache_bytes(int n) { return (size_t)std::min(n, kKeyCache) * sizeof(uint32_t); }
 
-template <typename K>
-cudaError_t allow_smem(K kern, size_t bytes) {
-  if (bytes <= 40 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-}
-
 }  // namespace
 
 size_t select_ws_bytes(const KParams& P, int batch, int max_ctx) {
@@ -414,20 +470,32 @@ size_t select_ws_bytes(const KParams& P, int batch, int max_ctx) {
 }
 
 cudaError_t launch_select(const KParams& P, const KCache& C, const void* q, int dtype, int k, int n_sink, int n_recent,
-                          int32_t* pages, int32_t* counts, void* ws, int max_ctx, cudaStream_t st) {
+                          int32_t* pages, int32_t* counts, void* ws, int max_ctx, int num_sms, cudaStream_t st) {
   const int np = std::max(1, max_ctx / kPage);
   uint32_t* keys = reinterpret_cast<uint32_t*>(ws);
-  const int pb = kScoreThreads / (P.d / 16) * kScorePages;
-  const dim3 grid((np + pb - 1) / pb, P.hkv, C.batch);
-  if (P.d == 128) page_score_kernel<128><<<grid, kScoreThreads, 0, st>>>(P, C, q, dtype, k, keys, np, max_ctx);
-  else page_score_kernel<256><<<grid, kScoreThreads, 0, st>>>(P, C, q, dtype, k, keys, np, max_ctx);
+  // about four blocks an SM: more rounds a block where there are more pages than that
+  const int pr = kScoreThreads / (P.d / 16) * kScorePages;
+  const long long blocks = (long long)((np + pr - 1) / pr) * P.hkv * C.batch;
+  const int rounds = (int)std::max(1LL, std::min(16LL, blocks / (4LL * num_sms)));
+  const dim3 grid((np + pr * rounds - 1) / (pr * rounds), P.hkv, C.batch);
+  if (P.d == 128) page_score_kernel<128><<<grid, kScoreThreads, 0, st>>>(P, C, q, dtype, k, keys, np, max_ctx, rounds);
+  else page_score_kernel<256><<<grid, kScoreThreads, 0, st>>>(P, C, q, dtype, k, keys, np, max_ctx, rounds);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const size_t dyn = key_cache_bytes(np);
-  if ((e = allow_smem(page_pick_kernel, dyn)) != cudaSuccess) return e;
-  page_pick_kernel<<<dim3(P.hkv, C.batch), kPickThreads, dyn, st>>>(C, P.hkv, keys, np, k, n_sink, n_recent, pages, counts,
-                                                                   max_ctx);
-  return cudaGetLastError();
+  if ((e = allow_dynamic_smem((const void*)page_pick_kernel, dyn)) != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};  // a programmatic dependent: placed while the scores drain
+  cfg.gridDim = dim3(P.hkv, C.batch);
+  cfg.blockDim = dim3(kPickThreads);
+  cfg.dynamicSmemBytes = dyn;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, page_pick_kernel, C, P.hkv, (const uint32_t*)keys, np, k, n_sink, n_recent, pages, counts, max_ctx);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_track(const KParams& P, const KCache& C, const float* scores, const float* lse, float* mass, int max_ctx,
@@ -446,19 +514,21 @@ int evict_ring_limit() { return 200 * 1024 / 16; }
 cudaError_t launch_evict(const KParams& P, const KCache& A, const KCache& B, const float* mass, float* mass_out, int budget,
                          int n_sink, int n_recent, int32_t* kept, void* ws, cudaStream_t st) {
   cudaError_t e;
-  if (A.ring > 0) {
-    // whole rows where the ring's rows fit 48 KB, else the widest slice of columns that does, at least 8
+  const bool apart = A.ring > 0 && A.win_k != B.win_k;
+  if (A.ring > 0 && !apart) {
+    // in place the windows go first, by the counters as they still are; whole rows where the ring's rows fit 48 KB,
+    // else the widest slice of columns that does, at least 8
     int cols = P.d;
     while (cols > 8 && (size_t)A.ring * cols * 2 > 48 * 1024) cols /= 2;
-    const size_t dyn = A.win_k == B.win_k ? (size_t)A.ring * cols * 2 : 0;
-    if ((e = allow_smem(evict_window_kernel, dyn)) != cudaSuccess) return e;
+    const size_t dyn = (size_t)A.ring * cols * 2;
+    if ((e = allow_dynamic_smem((const void*)evict_window_kernel, dyn)) != cudaSuccess) return e;
     evict_window_kernel<<<dim3((P.d + cols - 1) / cols, 2 * P.hkv, A.batch), 256, dyn, st>>>(A, B, P.hkv, P.d, budget, cols);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   const size_t dyn = key_cache_bytes(A.max_pages);
-  if ((e = allow_smem(evict_pick_kernel, dyn)) != cudaSuccess) return e;
-  evict_pick_kernel<<<A.batch, kPickThreads, dyn, st>>>(A, B, mass, mass_out, budget, n_sink, n_recent, kept,
-                                                       reinterpret_cast<int32_t*>(ws));
+  if ((e = allow_dynamic_smem((const void*)evict_pick_kernel, dyn)) != cudaSuccess) return e;
+  evict_pick_kernel<<<dim3(apart ? 1 + 2 * P.hkv : 1, A.batch), kPickThreads, dyn, st>>>(
+      A, B, mass, mass_out, budget, n_sink, n_recent, kept, reinterpret_cast<int32_t*>(ws), P.hkv, P.d);
   return cudaGetLastError();
 }
 
