@@ -214,20 +214,22 @@ static tq_status make_cache(const tq_cache* c, const KParams& K, KCache* C, bool
 
 // Decode workspace of either kind of layer (8-bit arm: pages and window in groups of 16 tokens).
 static WsLayout decode_layout(const KParams& K, int batch, int max_ctx, int n_splits) {
-  if (K.int8) return int8_ws_layout(K, batch, (long long)(max_ctx + TQ_PAGE_SIZE - 1) / TQ_PAGE_SIZE + 1, n_splits, num_sms());
+  if (K.int8) return int8_ws_layout(K, batch, 1, (long long)(max_ctx + TQ_PAGE_SIZE - 1) / TQ_PAGE_SIZE + 1, n_splits, num_sms());
   return decode_ws_layout(K, batch, max_ctx, n_splits, num_sms());
 }
 
 // Prefill workspace: the virtual sequences' counters and parent rows, then a decode workspace
 // for batch * n_query sequences.
 static size_t prefill_layout(const KParams& K, int batch, int n_query, int max_ctx, WsLayout* L) {
-  if (K.int8 && int8_prefill_tc_ok(K, n_query)) {
-    *L = int8_prefill_layout(K, batch, n_query, max_ctx, num_sms());
+  if (K.int8) {
+    *L = int8_prefill_tc_ok(K, n_query)
+             ? int8_prefill_layout(K, batch, n_query, max_ctx, num_sms())
+             : int8_ws_layout(K, batch, n_query, (long long)(max_ctx + TQ_PAGE_SIZE - 1) / TQ_PAGE_SIZE + 1, 0, num_sms());
     return L->total;
   }
   const size_t head = ((size_t)3 * batch * n_query * sizeof(int32_t) + 255) & ~(size_t)255;
-  const int S = !K.int8 && prefill_tiles_ok(K) ? prefill_tile_splits(K, batch, n_query, max_ctx, num_sms()) : 0;
-  *L = decode_layout(K, batch * n_query, max_ctx, S);
+  const int S = prefill_tiles_ok(K) ? prefill_tile_splits(K, batch, n_query, max_ctx, num_sms()) : 0;
+  *L = decode_ws_layout(K, batch * n_query, max_ctx, S, num_sms());
   return head + L->total;
 }
 
@@ -362,7 +364,7 @@ extern "C" tq_status tq_decode_attention(const tq_layer_params* p, const tq_cach
   }
   if (K.int8)
     return cuda_status(launch_int8_decode(K, C, q, dtype, scale, nullptr, nullptr, 0, out, lse, scores, workspace, L, max_ctx,
-                                          reinterpret_cast<cudaStream_t>(stream)),
+                                          1, 0, reinterpret_cast<cudaStream_t>(stream)),
                        "tq_decode_attention");
   return cuda_status(launch_decode(K, C, q, dtype, scale, out, lse, scores, workspace, L, max_ctx,
                                    reinterpret_cast<cudaStream_t>(stream)),
@@ -400,7 +402,11 @@ extern "C" tq_status tq_prefill_attention(const tq_layer_params* p, const tq_cac
     return TQ_ERR_CAPACITY;
   }
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (K.int8 && int8_prefill_tc_ok(K, n_query)) {
+  if (K.int8) {
+    if (!int8_prefill_tc_ok(K, n_query))
+      return cuda_status(launch_int8_decode(K, C, q, dtype, scale, nullptr, nullptr, 0, out, lse, nullptr, workspace, L, max_ctx,
+                                            n_query, n_query, st),
+                         "tq_prefill_attention");
     if ((long long)cache->batch * L.n_comp_splits > 65535)
       return fail(TQ_ERR_INVALID_ARG, "batch times splits must be <= 65535");
     return cuda_status(launch_int8_prefill(K, C, n_query, q, dtype, scale, out, lse, workspace, L, max_ctx, st),
@@ -418,9 +424,6 @@ extern "C" tq_status tq_prefill_attention(const tq_layer_params* p, const tq_cac
   V.n_compressed = nc_v;
   V.parent = parent;
   V.batch = (int)nv;
-  if (K.int8)
-    return cuda_status(launch_int8_decode(K, V, q, dtype, scale, nullptr, nullptr, 0, out, lse, nullptr, dws, L, max_ctx, st),
-                       "tq_prefill_attention");
   if (prefill_tiles_ok(K))
     return cuda_status(launch_prefill_tiles(K, V, n_query, cache->batch, q, dtype, scale, out, lse, dws, L, max_ctx, st),
                        "tq_prefill_attention");
@@ -509,7 +512,7 @@ extern "C" tq_status tq_select_pages(const tq_layer_params* p, const tq_cache* c
 }
 
 static WsLayout pages_layout(const KParams& K, int batch, int n_sel, int n_splits) {
-  return int8_ws_layout(K, batch, (long long)n_sel + (K.window + 2 * TQ_PAGE_SIZE - 2) / TQ_PAGE_SIZE, n_splits, num_sms());
+  return int8_ws_layout(K, batch, 1, (long long)n_sel + (K.window + 2 * TQ_PAGE_SIZE - 2) / TQ_PAGE_SIZE, n_splits, num_sms());
 }
 
 extern "C" size_t tq_decode_pages_workspace_size(const tq_layer_params* p, int batch, int n_sel, int n_splits) {
@@ -546,7 +549,7 @@ extern "C" tq_status tq_decode_attention_pages(const tq_layer_params* p, const t
     return TQ_ERR_CAPACITY;
   }
   return cuda_status(launch_int8_decode(K, C, q, dtype, scale, pages, counts, n_sel, out, lse, nullptr, workspace, L, max_ctx,
-                                        reinterpret_cast<cudaStream_t>(stream)),
+                                        1, 0, reinterpret_cast<cudaStream_t>(stream)),
                      "tq_decode_attention_pages");
 }
 

@@ -2,7 +2,8 @@
 //
 //   l_t = scale ks <q, c_t> (pages), scale <q, k_t> (float16 window);  out = sum_t p_t vs cv_t / sum_t p_t.
 //
-// The G <= 8 query heads of a KV head share every load.  Both products run on mma.m16n8k16 with
+// The G <= 8 query heads of a KV head share every load; of a chunk of queries (prefill attention where the tcgen05
+// kernel does not apply) so do the heads of 8 / G queries, each row with its own causal length.  Both products run on mma.m16n8k16 with
 // operands exact in f16: the codes as they are (integers up to 127), the query and the softmax weights
 // as f16 hi + lo limbs in rows h and h + 8 of the 16-row tile (22 bits; a single f16 limb would leave
 // 2^-12 of the float output, and with G <= 8 the second limb fills rows that were empty).  A query row is
@@ -91,10 +92,10 @@ struct Shared {
 };
 
 // Row scale (a power of two that brings the largest magnitude into [2^13, 2^14)) and operand fragments of
-// the G query rows at q [G][dh]: a warp holds two rows in registers, four channels a lane (eight at d = 256), so that
+// R query rows, row(h) [dh] each: a warp holds two rows in registers, four channels a lane (eight at d = 256), so that
 // the loads of all rows are in flight at once.  All threads; ends with a barrier.
-template <int D>
-__device__ void load_query(Shared<D>& sh, const void* q, int dtype, size_t row0, int G, int dh) {
+template <int D, typename Row>
+__device__ void load_query(Shared<D>& sh, const void* q, int dtype, Row row, int rows, int dh) {
   constexpr int Q = D / 128, R = 8 / kWarps;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   float x[R][Q][4];
@@ -104,7 +105,7 @@ __device__ void load_query(Shared<D>& sh, const void* q, int dtype, size_t row0,
     for (int i = 0; i < Q; ++i) {
       const int h = warp + kWarps * r, c = 128 * i + 4 * lane;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) x[r][i][e] = h < G && c < dh ? load_elem(q, dtype, (long long)((row0 + h) * dh + c + e)) : 0.f;
+      for (int e = 0; e < 4; ++e) x[r][i][e] = h < rows && c < dh ? load_elem(q, dtype, (long long)(row(h) * dh + c + e)) : 0.f;
     }
 #pragma unroll
   for (int r = 0; r < R; ++r) {
@@ -133,23 +134,29 @@ __device__ void load_query(Shared<D>& sh, const void* q, int dtype, size_t row0,
 
 // Work of one (sequence, KV head): its pages (all in order, or a list's), then the window in groups of 16.
 struct Items {
-  int n, nc, np, nwin, pages, total;
+  int len;                       // of the sequence
+  int n, nc, np, nwin;           // what is seen of it: tokens, of them in pages, those pages, in the window
+  int pages, total;
   bool bad;
 };
 
-__device__ __forceinline__ Items items_of(const KCache& C, int hkv, const int32_t* counts, int n_sel, int max_ctx, int b, int g) {
+// What query i1 - 1 of the last n_query tokens sees (a decode step: query 0 of 1); least: the shortest valid sequence.
+__device__ __forceinline__ Items items_of(const KCache& C, int hkv, const int32_t* counts, int n_sel, int max_ctx, int b, int g,
+                                          int n_query, int i1, int least) {
   Items it;
-  it.n = C.seq_len[b];
-  it.nc = C.n_compressed[b];
-  it.bad = it.n < 0 || it.n > max_ctx || it.nc < 0 || it.nc > it.n;
-  it.n = min(max(it.n, 0), max_ctx);
-  it.nc = min(max(it.nc, 0), it.n);
+  int n = C.seq_len[b], nc = C.n_compressed[b];
+  it.bad = n < least || n > max_ctx || nc < 0 || nc > n;
+  n = min(max(n, 0), max_ctx);
+  nc = min(max(nc, 0), n);
+  it.bad |= n - nc >= C.ring;
+  n = min(n, nc + C.ring - 1);
+  it.len = n;
+  it.n = max(0, n - n_query + i1);
+  it.nc = min(nc, it.n);
   it.np = (it.nc + kPage - 1) / kPage;
-  it.nwin = it.n - it.nc;
-  // positions from nc on are in the ring; a virtual sequence's nc is its parent's clipped to what it sees
-  it.bad |= it.np > C.max_pages || it.nwin >= C.ring;
+  it.bad |= it.np > C.max_pages;
   it.np = min(it.np, C.max_pages);
-  it.nwin = min(it.nwin, C.ring - 1);
+  it.nwin = it.n - it.nc;
   it.pages = it.np;
   if (counts) {
     it.pages = counts[(size_t)b * hkv + g];
@@ -164,7 +171,7 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
     i8_decode_kernel(const __grid_constant__ KParams P, const __grid_constant__ KCache C, const void* q, int dtype,
                      float scale, const int32_t* __restrict__ pages, const int32_t* __restrict__ counts, int n_sel,
-                     float* out, float* lse, float* scores, unsigned char* ws, WsLayout L, int max_ctx) {
+                     float* out, float* lse, float* scores, unsigned char* ws, WsLayout L, int max_ctx, int n_query, int least) {
   constexpr int J = D / 64;
   __shared__ Shared<D> sh;
   extern __shared__ __align__(128) unsigned char dyn[];  // [kWarps][kRing] pages, at the end [kWarps][8][D] floats
@@ -180,11 +187,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
   uint32_t fly = 0, phase = 0;  // bit: a copy is in flight into the slot; the parity it ends
   int slot = 0;
 
-  const int b = blockIdx.z, g = blockIdx.y, s = blockIdx.x;
-  const size_t head0 = (size_t)b * P.hq + (size_t)g * G;
-  const int cb = C.parent ? C.parent[b] : b;
-  const Items it = items_of(C, P.hkv, counts, n_sel, max_ctx, b, g);
+  // rows: the heads of `qs_here` queries from q0 on, row h is head h % G of query q0 + h / G
+  const int pack = TQ_MAX_GQA / G, parts = (n_query + pack - 1) / pack;
+  const int b = blockIdx.z / parts, q0 = blockIdx.z % parts * pack, g = blockIdx.y, s = blockIdx.x;
+  const int R = G * min(pack, n_query - q0);
+  auto row_of = [&](int h) { return ((size_t)b * n_query + q0 + h / G) * P.hq + (size_t)g * G + h % G; };
+  const Items it = items_of(C, P.hkv, counts, n_sel, max_ctx, b, g, n_query, q0 + R / G, least);
   if (it.bad && s == 0 && tid == 0) atomicOr(&g_int8_decode_err, TQ_DEVERR_SEQ_LEN);
+  const int seen0 = it.len - n_query + q0 + 1, seen = seen0 + g8 / G;  // tokens that the first query and row g8 see
   const int per = (it.total + S - 1) / S, i0 = min(it.total, s * per), i1 = min(it.total, i0 + per);
   const int32_t* list = pages ? pages + ((size_t)b * P.hkv + g) * n_sel : nullptr;
   const int ip = min(i1, it.pages);  // pages [i0, ip)
@@ -197,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
     if (k0 + lane < mine) {
       const int i = i0 + warp + kWarps * (k0 + lane);
       o = list ? list[i] : i;
-      if (o >= 0 && o < it.np) p = C.block_table[(size_t)cb * C.max_pages + o];
+      if (o >= 0 && o < it.np) p = C.block_table[(size_t)b * C.max_pages + o];
       if (p < 0 || p >= C.n_pages) {
         atomicOr(&g_int8_decode_err, TQ_DEVERR_PAGE_INDEX);
         p = -1;
@@ -226,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
     }
   }
 
-  load_query<D>(sh, q, dtype, head0, G, P.dh);
+  load_query<D>(sh, q, dtype, row_of, R, P.dh);
   const float qs = sh.unscale[g8] * scale * kLog2e;  // scores in powers of two
 
   float acc[J][2][4][4];
@@ -249,14 +259,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
     for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) x[nt][e] = (sacc[nt][e] + sacc[nt][e + 2]) * f;
-    if (pos0 + kPage > live_to || scores) {
+    if (pos0 + kPage > min(live_to, seen0) || scores) {
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int pos = pos0 + 4 * t4 + 2 * nt + e;
-          if (pos >= live_to) x[nt][e] = -INFINITY;
-          else if (scores && g8 < G) scores[(head0 + g8) * (size_t)max_ctx + pos] = x[nt][e] * kLn2;
+          if (pos >= min(live_to, seen)) x[nt][e] = -INFINITY;
+          else if (scores && g8 < R) scores[row_of(g8) * (size_t)max_ctx + pos] = x[nt][e] * kLn2;
         }
     }
     float mx = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
@@ -359,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
 #pragma unroll 1
     for (; i < i1; i += kWarps) {
       const int pos0 = it.nc + (i - it.pages) * kPage, live_to = it.nc + it.nwin;
-      const __half* kring = C.win_k + ((size_t)cb * P.hkv + g) * C.ring * D;
+      const __half* kring = C.win_k + ((size_t)b * P.hkv + g) * C.ring * D;
       float sacc[2][4] = {};
 #pragma unroll
       for (int nt = 0; nt < 2; ++nt) {
@@ -379,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
         }
       }
       const uint4 a = softmax(sacc, qs, 1.f, pos0, live_to);
-      const __half* vring = C.win_v + ((size_t)cb * P.hkv + g) * C.ring * D;
+      const __half* vring = C.win_v + ((size_t)b * P.hkv + g) * C.ring * D;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         uint32_t r[4][4];
@@ -419,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
             make_float4((acc[j][h][0][c] + acc[j][h][0][c + 2]) * undo, (acc[j][h][1][c] + acc[j][h][1][c + 2]) * undo,
                         (acc[j][h][2][c] + acc[j][h][2][c + 2]) * undo, (acc[j][h][3][c] + acc[j][h][3][c + 2]) * undo);
   __syncthreads();
-  for (int i = tid; i < G * D; i += kThreads) {
+  for (int i = tid; i < R * D; i += kThreads) {
     const int h = i / D, j = i % D;
     float M = sh.m[0][h];
 #pragma unroll
@@ -434,10 +444,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
     }
     if (S == 1) {
       // nothing visible: 0 and -inf; a NaN sum passes through
-      if (j < P.dh) out[(head0 + h) * P.dh + j] = sum == 0.f ? 0.f : o / sum;
-      if (lse && j == 0) lse[head0 + h] = sum == 0.f ? -INFINITY : M * kLn2 + logf(sum);
+      if (j < P.dh) out[row_of(h) * P.dh + j] = sum == 0.f ? 0.f : o / sum;
+      if (lse && j == 0) lse[row_of(h)] = sum == 0.f ? -INFINITY : M * kLn2 + logf(sum);
     } else {
-      const size_t row = (head0 + h) * S + s;
+      const size_t row = row_of(h) * S + s;
       reinterpret_cast<float*>(ws + L.acc)[row * D + j] = o;
       if (j == 0) reinterpret_cast<float2*>(ws + L.ml)[row] = make_float2(M, sum);
     }
@@ -504,15 +514,16 @@ cudaError_t launch_after(void (*kern)(K...), dim3 grid, int threads, cudaStream_
 template <int D>
 cudaError_t decode(const KParams& P, const KCache& C, const void* q, int dtype, float scale, const int32_t* pages,
                    const int32_t* counts, int n_sel, float* out, float* lse, float* scores, unsigned char* ws,
-                   const WsLayout& L, int max_ctx, cudaStream_t st) {
+                   const WsLayout& L, int max_ctx, int n_query, int least, cudaStream_t st) {
   const size_t dyn = std::max((size_t)kWarps * kRing * raw_bytes(D), (size_t)kWarps * 8 * D * sizeof(float));
   cudaError_t e = allow_dynamic_smem((const void*)i8_decode_kernel<D>, dyn);
   if (e != cudaSuccess) return e;
-  i8_decode_kernel<D><<<dim3(L.n_comp_splits, P.hkv, C.batch), kThreads, dyn, st>>>(P, C, q, dtype, scale, pages, counts, n_sel,
-                                                                                out, lse, scores, ws, L, max_ctx);
+  const int pack = TQ_MAX_GQA / P.G, parts = (n_query + pack - 1) / pack;
+  i8_decode_kernel<D><<<dim3(L.n_comp_splits, P.hkv, C.batch * parts), kThreads, dyn, st>>>(
+      P, C, q, dtype, scale, pages, counts, n_sel, out, lse, scores, ws, L, max_ctx, n_query, least);
   e = cudaGetLastError();
   if (e != cudaSuccess || L.n_comp_splits == 1) return e;
-  return launch_int8_combine(P, ws, L, C.batch, out, lse, st);
+  return launch_int8_combine(P, ws, L, (long long)C.batch * n_query, out, lse, st);
 }
 
 }  // namespace
@@ -522,18 +533,19 @@ cudaError_t decode(const KParams& P, const KCache& C, const void* q, int dtype, 
 // waves, since few splits of unequal sequences leave a long tail (32 x 8192 tokens, 8 heads: 2 or 3 splits 103 us, 5
 // splits 93 us).  A split keeps a group for each of its warps.  (Blocks that share all sequences' groups evenly in
 // one wave were no faster, 95 us, and would make a sequence's rounding depend on the others in its batch.)
-WsLayout int8_ws_layout(const KParams& P, int batch, long long max_items, int n_splits, int num_sms) {
+WsLayout int8_ws_layout(const KParams& P, int batch, int n_query, long long max_items, int n_splits, int num_sms) {
   WsLayout L{};
   long long S = n_splits;
   if (S <= 0) {
-    const long long units = std::max(1LL, (long long)batch * P.hkv), slots = (long long)ctas_per_sm(P.d) * num_sms;
+    const int pack = TQ_MAX_GQA / P.G;
+    const long long units = (long long)batch * ((n_query + pack - 1) / pack) * P.hkv, slots = (long long)ctas_per_sm(P.d) * num_sms;
     S = slots / units;
     if (S < 4) S = (2 * slots + units - 1) / units;
     S = std::min(S, (max_items + kWarps - 1) / kWarps);
   }
   S = std::max(1LL, std::min(S, std::min(max_items, 65535LL)));
   L.n_comp_splits = (int)S;
-  const size_t heads = (size_t)batch * P.hq;
+  const size_t heads = (size_t)batch * n_query * P.hq;
   size_t o = 0;
   if (S > 1) {
     L.ml = o;
@@ -547,11 +559,11 @@ WsLayout int8_ws_layout(const KParams& P, int batch, long long max_items, int n_
 
 cudaError_t launch_int8_decode(const KParams& P, const KCache& C, const void* q, int dtype, float scale, const int32_t* pages,
                                const int32_t* counts, int n_sel, float* out, float* lse, float* scores, void* ws,
-                               const WsLayout& L, int max_ctx, cudaStream_t st) {
+                               const WsLayout& L, int max_ctx, int n_query, int least, cudaStream_t st) {
   unsigned char* w = reinterpret_cast<unsigned char*>(ws);
   if (P.d == 128)
-    return decode<128>(P, C, q, dtype, scale, pages, counts, n_sel, out, lse, scores, w, L, max_ctx, st);
-  return decode<256>(P, C, q, dtype, scale, pages, counts, n_sel, out, lse, scores, w, L, max_ctx, st);
+    return decode<128>(P, C, q, dtype, scale, pages, counts, n_sel, out, lse, scores, w, L, max_ctx, n_query, least, st);
+  return decode<256>(P, C, q, dtype, scale, pages, counts, n_sel, out, lse, scores, w, L, max_ctx, n_query, least, st);
 }
 
 cudaError_t launch_int8_combine(const KParams& P, const unsigned char* ws, const WsLayout& L, long long rows, float* out,

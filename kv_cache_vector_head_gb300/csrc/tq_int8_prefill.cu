@@ -783,8 +783,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-// Rows of a block's query tile: two tiles of 128.
-bool int8_prefill_tc_ok(const KParams& P, int n_query) { return P.d == D && (long long)n_query * P.G > 16; }
+// From 49 rows a KV head on: up to there the decode kernel, eight rows a block, is as fast or faster (8 sequences of 8192
+// tokens, 8 heads: 48 rows 106 us, here 122 us; 64 rows 133 and 126 us; one of 32768 tokens, G = 8: 48 rows 70 and 60 us).
+bool int8_prefill_tc_ok(const KParams& P, int n_query) { return P.d == D && (long long)n_query * P.G > 48; }
 
 // Blocks' rows a KV head, and the places of the gathered sums (afrag) and of the partial results in `splits` splits;
 // returns the bytes they take.

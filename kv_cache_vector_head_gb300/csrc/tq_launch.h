@@ -59,17 +59,18 @@ cudaError_t launch_int8_read(const KParams& P, const KCache& C, void* k, void* v
                              cudaStream_t st);
 
 // Decode of the 8-bit arm over at most max_items groups of 16 tokens a sequence; pages / counts: the page
-// ordinals of every (sequence, KV head), n_sel a row, or null for all pages.
-WsLayout int8_ws_layout(const KParams& P, int batch, long long max_items, int n_splits, int num_sms);
+// ordinals of every (sequence, KV head), n_sel a row, or null for all pages.  n_query > 1: the last n_query tokens' queries,
+// each seeing what is before it and itself.  Sequences shorter than `least` are flagged.
+WsLayout int8_ws_layout(const KParams& P, int batch, int n_query, long long max_items, int n_splits, int num_sms);
 cudaError_t launch_int8_decode(const KParams& P, const KCache& C, const void* q, int dtype, float scale, const int32_t* pages,
                                const int32_t* counts, int n_sel, float* out, float* lse, float* scores, void* ws,
-                               const WsLayout& L, int max_ctx, cudaStream_t st);
+                               const WsLayout& L, int max_ctx, int n_query, int least, cudaStream_t st);
 
 // Joins the splits of rows x hq query rows (L.ml, L.acc) in their order; references in powers of two.
 cudaError_t launch_int8_combine(const KParams& P, const unsigned char* ws, const WsLayout& L, long long rows, float* out,
                                 float* lse, cudaStream_t st);
 
-// Prefill attention of the 8-bit arm on tcgen05 (d = 128, more than 16 rows a KV head).
+// Prefill attention of the 8-bit arm on tcgen05 (d = 128, more than 48 rows a KV head).
 bool int8_prefill_tc_ok(const KParams& P, int n_query);
 WsLayout int8_prefill_layout(const KParams& P, int batch, int n_query, int max_ctx, int num_sms);
 cudaError_t launch_int8_prefill(const KParams& P, const KCache& C, int n_query, const void* q, int dtype, float scale,

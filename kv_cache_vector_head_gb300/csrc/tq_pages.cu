@@ -21,6 +21,7 @@ namespace {
 
 constexpr int kPickThreads = 1024;
 constexpr int kPickWarps = kPickThreads / 32;
+constexpr int kStageTable = 4096;  // tables up to this long are put together in shared memory (48 KB with their keys)
 constexpr int kKeyCache = 40960;  // keys kept in shared memory (160 KB); longer lists are re-read from L2
 
 // Order-preserving map of a float to an unsigned integer (-0 counts as 0, NaN as the least).
@@ -430,7 +431,8 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
     }
     return;
   }
-  int32_t* wt = ws + (size_t)b * 2 * mp;
+  // (short tables: in shared memory, behind the keys)
+  int32_t* wt = mp <= kStageTable ? reinterpret_cast<int32_t*>(cache) + mp : ws + (size_t)b * 2 * mp;
   float* wm = reinterpret_cast<float*>(wt + mp);
   const int part = nc % kPage ? 1 : 0;  // a partly filled page stays behind the kept ones
   pick(sh, cache, np, keep, n_sink, n_recent, [&](int i) { return order_key(m[i]); },
@@ -525,7 +527,7 @@ cudaError_t launch_evict(const KParams& P, const KCache& A, const KCache& B, con
     evict_window_kernel<<<dim3((P.d + cols - 1) / cols, 2 * P.hkv, A.batch), 256, dyn, st>>>(A, B, P.hkv, P.d, budget, cols);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  const size_t dyn = key_cache_bytes(A.max_pages);
+  const size_t dyn = key_cache_bytes(A.max_pages) + (A.max_pages <= kStageTable ? (size_t)A.max_pages * 8 : 0);
   if ((e = allow_dynamic_smem((const void*)evict_pick_kernel, dyn)) != cudaSuccess) return e;
   evict_pick_kernel<<<dim3(apart ? 1 + 2 * P.hkv : 1, A.batch), kPickThreads, dyn, st>>>(
       A, B, mass, mass_out, budget, n_sink, n_recent, kept, reinterpret_cast<int32_t*>(ws), P.hkv, P.d);
