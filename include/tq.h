@@ -250,7 +250,7 @@ tq_status tq_quantize_values(const tq_layer_params* p, const void* v, tq_dtype d
  * codes uint32 [16][d key_bits / 32] (code j of a token at bits
  * (j b) mod 32 of word (j b) / 32), value scales float16 [16], value zeros
  * float16 [16], value codes uint32 [16][d value_bits / 32].
- * 8-bit arm (int8 = 1): int8 [d] smallest and int8 [d] largest key code of each
+ * 8-bit arm (int8 = 1; the float16 rings 16-byte aligned): int8 [d] smallest and int8 [d] largest key code of each
  * channel, float key scale, float value scale, 24 zero bytes, then the codes as
  * code + 128 in a byte, in tensor-core operand order:
  *   keys   uint8 [2 n][d/64 j][8 g][4 t][16 e]     token 4 (g / 2) + 2 n + g mod 2,
@@ -345,7 +345,7 @@ size_t tq_decode_workspace_size(const tq_layer_params* p, int batch, int max_ctx
  *   p = softmax(l) over all seq_len[b] tokens; lse = log sum exp(l).
  *   q        [device] [batch][Hq][head_dim] in dtype
  *   scale    softmax scale (usually 1/sqrt(d))
- *   out      [device] out, float [batch][Hq][head_dim]
+ *   out      [device] out, float [batch][Hq][head_dim] (8-bit arm: 16-byte aligned)
  *   lse      [device] out, nullable, float [batch][Hq]
  *   scores   [device] out, nullable, float [batch][Hq][max_ctx]: every l_i
  *            at its token position (for inspection; costs extra stores)
@@ -404,7 +404,7 @@ tq_status tq_decode_attention_static(const tq_layer_params* p, const tq_cache* c
  * pass (query tiles); other layers run the decode pipeline over the virtual
  * sequences.  The workspace size accounts for either.
  *   q         [device] [batch][n_query][Hq][head_dim] in dtype
- *   out       [device] out, float [batch][n_query][Hq][head_dim]
+ *   out       [device] out, float [batch][n_query][Hq][head_dim] (8-bit arm: 16-byte aligned)
  *   lse       [device] out, float [batch][n_query][Hq] (nullable)
  *   workspace [device] 256-byte aligned, >= tq_prefill_workspace_size bytes
  *   max_ctx   upper bound of seq_len over the batch

@@ -198,6 +198,8 @@ static tq_status make_cache(const tq_cache* c, const KParams& K, KCache* C, bool
   if (!c->block_table || !c->seq_len || !c->n_compressed) return fail(TQ_ERR_INVALID_ARG, "null block_table / counters");
   if (need_window && K.window > 0 && (!c->win_k || !c->win_v))
     return fail(TQ_ERR_INVALID_ARG, "window > 0 needs win_k and win_v");
+  if (need_window && K.int8 && (!aligned(c->win_k, 16) || !aligned(c->win_v, 16)))
+    return fail(TQ_ERR_INVALID_ARG, "int8: win_k and win_v must be 16-byte aligned");
   C->pool = reinterpret_cast<unsigned char*>(c->page_pool);
   C->n_pages = c->n_pages;
   C->block_table = c->block_table;
@@ -356,6 +358,7 @@ extern "C" tq_status tq_decode_attention(const tq_layer_params* p, const tq_cach
   if (!aligned(workspace, 256)) return fail(TQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   if (max_ctx < 0 || n_splits < 0) return fail(TQ_ERR_INVALID_ARG, "max_ctx and n_splits must be >= 0");
   if (!(scale == scale)) return fail(TQ_ERR_INVALID_ARG, "scale is NaN");
+  if (K.int8 && !aligned(out, 16)) return fail(TQ_ERR_INVALID_ARG, "int8: out must be 16-byte aligned");
   if (!decode_rows_ok(K, cache->batch)) return fail(TQ_ERR_INVALID_ARG, "batch must be <= 65535 and batch * G <= 262140");
   const WsLayout L = decode_layout(K, cache->batch, max_ctx, n_splits);
   if (workspace_bytes < L.total) {
@@ -395,6 +398,7 @@ extern "C" tq_status tq_prefill_attention(const tq_layer_params* p, const tq_cac
   if (!aligned(workspace, 256)) return fail(TQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   if (max_ctx < 0) return fail(TQ_ERR_INVALID_ARG, "max_ctx must be >= 0");
   if (!(scale == scale)) return fail(TQ_ERR_INVALID_ARG, "scale is NaN");
+  if (K.int8 && !aligned(out, 16)) return fail(TQ_ERR_INVALID_ARG, "int8: out must be 16-byte aligned");
   WsLayout L;
   const size_t need = prefill_layout(K, cache->batch, n_query, max_ctx, &L);
   if (workspace_bytes < need) {
@@ -542,6 +546,7 @@ extern "C" tq_status tq_decode_attention_pages(const tq_layer_params* p, const t
   if (!aligned(workspace, 256)) return fail(TQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   if (max_ctx < 0 || n_splits < 0 || n_sel < 1) return fail(TQ_ERR_INVALID_ARG, "max_ctx, n_splits >= 0 and n_sel >= 1");
   if (!(scale == scale)) return fail(TQ_ERR_INVALID_ARG, "scale is NaN");
+  if (K.int8 && !aligned(out, 16)) return fail(TQ_ERR_INVALID_ARG, "int8: out must be 16-byte aligned");
   if (!decode_rows_ok(K, cache->batch)) return fail(TQ_ERR_INVALID_ARG, "batch must be <= 65535 and batch * G <= 262140");
   const WsLayout L = pages_layout(K, cache->batch, n_sel, n_splits);
   if (workspace_bytes < L.total) {

@@ -103,6 +103,16 @@ __device__ __forceinline__ uint32_t i8_hi2(uint32_t w) {
   return *reinterpret_cast<uint32_t*>(&h);
 }
 
+// Factor of a page's weights: value scale vs times 2^d (d: by how much the exponents' reference is above the weights'),
+// times top.  Kept finite: where d passes 126 or the product 2^100 the weights it meets are 2^-92 or less of the largest,
+// and may be 0, which infinity would turn into NaN.
+__device__ __forceinline__ float i8_weight_factor(float vs, float two_d, float top) { return fminf(vs * two_d, 1.2676506e30f) * top; }
+__device__ __forceinline__ float i8_two_to(float d) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fminf(d, 126.f)));
+  return y;
+}
+
 // Elements 2 i, 2 i + 1 of a 16-byte piece (bf16 or f16), or i of four floats.
 template <typename T>
 __device__ __forceinline__ float elem_of(const uint4& w, int i);

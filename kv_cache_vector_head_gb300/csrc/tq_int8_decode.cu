@@ -7,9 +7,9 @@
 // operands exact in f16: the codes as they are (integers up to 127), the query and the softmax weights
 // as f16 hi + lo limbs in rows h and h + 8 of the 16-row tile (22 bits; a single f16 limb would leave
 // 2^-12 of the float output, and with G <= 8 the second limb fills rows that were empty).  A query row is
-// scaled by a power of two so that its limbs keep clear of f16's subnormals; the pages' value scales
-// ride on the weights relative to a power of two that bounds the scales seen so far, adjusted with
-// the running maximum.
+// scaled by a power of two so that its limbs keep clear of f16's subnormals; the pages' value scales ride on the
+// weights, which have a reference of their own, the largest p vs so far (the exponents' is the largest p): a page of
+// large values that hardly weighs does not push the others' weights under f16's range.
 //
 // The page holds its codes in operand order, so a lane's 16 bytes are four operands and the scores come out
 // of the first product in the layout the second one takes them: a warp carries a page from its codes to the
@@ -74,14 +74,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-
-// Smallest power of two >= s (s a page scale: 0 or normal)
-__device__ __forceinline__ float pow2_above(float s) {
-  return __uint_as_float((__float_as_uint(s) + 0x007fffffu) & 0x7f800000u);
-}
-
-// 1 / v for a power of two v between 2^-126 and 2^126
-__device__ __forceinline__ float pow2_inv(float v) { return __uint_as_float(0x7f000000u - __float_as_uint(v)); }
 
 template <int D>
 struct Shared {
@@ -248,7 +240,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[j][h][i][r] = 0.f;
-  float m = -INFINITY, l = 0.f, vref = 0.f;  // of head g8 (l: this lane's tokens)
+  // of row g8, in powers of two: the largest score, and relative to it the largest score times value scale (l: this
+  // lane's tokens)
+  float m = -INFINITY, wref = -INFINITY, l = 0.f;
 
   // products -> scores (times f) -> weights in operand order; the running state and the accumulators follow.
   // Tokens pos0 .. of which those before live_to count.
@@ -273,16 +267,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
     const float mn = fmaxf(m, mx);
-    const float vn = fmaxf(vref, pow2_above(vs));
     // a score that is NaN leaves mn as it was and makes its weights NaN
     const float mb = mn == -INFINITY ? 0.f : mn;
-    const float vi = vn > 0.f ? pow2_inv(vn) : 0.f;
-    if (__any_sync(0xffffffffu, mn != m || vn != vref)) {
-      const float al = ex2(m - mb);  // 0 before the first score
-      const float av = vn > 0.f ? al * (vref * vi) : al;
+    const float wr = mn == m ? wref : wref - (mn - m), wn = fmaxf(wr, (mx - mb) + __log2f(vs));
+    if (__any_sync(0xffffffffu, mn != m || wn != wr)) {
+      l *= ex2(m - mb);  // 0 before the first score
+      const float av = wn == -INFINITY ? 0.f : ex2(wr - wn);
       m = mn;
-      vref = vn;
-      l *= al;
+      wref = wn;
 #pragma unroll
       for (int j = 0; j < J; ++j)
 #pragma unroll
@@ -292,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
 #pragma unroll
             for (int r = 0; r < 4; ++r) acc[j][h][i4][r] *= av;
     }
-    const float wv = vs * vi * kWeightTop;
+    const float wv = wn == -INFINITY ? 0.f : i8_weight_factor(vs, i8_two_to(-wn), kWeightTop);
     float p[2][2];
 #pragma unroll
     for (int nt = 0; nt < 2; ++nt)
@@ -415,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
     sh.m[warp][g8] = m;
     sh.l[warp][g8] = l;
   }
-  const float undo = vref * (1.f / kWeightTop);
+  const float undo = wref == -INFINITY ? 0.f : ex2(wref) * (1.f / kWeightTop);
   float* merge = reinterpret_cast<float*>(dyn);
   __syncthreads();  // every warp's ring is idle
   float* box = merge + ((size_t)warp * 8 + g8) * D;

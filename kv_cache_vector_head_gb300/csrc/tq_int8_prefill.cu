@@ -9,7 +9,7 @@
 //
 //   warps 0-7, 8-15  a unit each, two threads a row: each takes its half of the S row from tensor memory
 //                    (tcgen05.ld), the halves agree on the reference of the exponents, and write P's limbs over S.
-//                    The reference follows the running maximum only when that has grown by 2^8, so O stays as it is in
+//                    The references follow the running maxima only when those have grown by 2^8, so O stays as it is in
 //                    almost every tile.  O is added to memory (scratch, in L2) and begun anew every four
 //                    tiles: the tensor cores' accumulation truncates, 2^-25 of O a step; over the whole of a long
 //                    context that would be 1e-5, over four tiles it is under 1e-6.  (O in registers instead, added
@@ -60,10 +60,11 @@ struct Shared {
   uint64_t sfull[2], pready[2], ofull[2], drained;
   uint64_t rawk[GROUPS], rawv[GROUPS];
   float2 scale[4][GROUPS];  // tile modulo 4: key and value scale of a group of 16 tokens
+  float vlog[4][GROUPS];    // log2 of the value scale
   uint32_t live[4];         // groups whose page is there; 8 bits on, groups with bad tokens
   uint32_t bad[4][GROUPS];  // window tokens with non-finite values
   float rowscale[256];            // 1 / the power of two of a query row
-  float mx[2][2][2][128];         // tile parity, unit, half: largest score of a row's half
+  float2 mx[2][2][2][128];  // tile parity, unit, half: a row's half's largest score and score times value scale
   float l[2][2][128];
   uint32_t tmem;
 };
@@ -138,9 +139,6 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-__device__ __forceinline__ float pow2_above(float s) { return __uint_as_float((__float_as_uint(s) + 0x007fffffu) & 0x7f800000u); }
-__device__ __forceinline__ float pow2_inv(float v) { return __uint_as_float(0x7f000000u - __float_as_uint(v)); }
-
 __device__ __forceinline__ uint64_t pair2(float a, float b) {
   uint64_t r;
   asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
@@ -179,11 +177,12 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return r;
 }
 
-// Largest score (powers of two) of a row's 64 columns at ts; sc: the four groups' scales.  FULL: all are visible and there;
-// else columns 0 .. see of the groups in `live`.
+// Largest score (powers of two) of a row's 64 columns at ts, and relative to it the largest score times value scale; sc,
+// vlog: the four groups' scales.
+// FULL: all are visible and there; else columns 0 .. see of the groups in `live`.
 template <bool FULL>
-__device__ __forceinline__ float largest(uint32_t ts, const float2* sc, float fq, int see, uint32_t live) {
-  float mx = -INFINITY;
+__device__ __forceinline__ float2 largest(uint32_t ts, const float2* sc, const float* vlog, float fq, int see, uint32_t live) {
+  float mx = -INFINITY, t[4];
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
     uint32_t v[2][16];
@@ -205,22 +204,27 @@ __device__ __forceinline__ float largest(uint32_t ts, const float2* sc, float fq
         a1 = max3(a1, x[2], x[3]);
       }
       // (-inf times a scale of 0 is NaN, which fmaxf leaves out)
-      mx = fmaxf(mx, fmaxf(a0, a1) * (sc[gi].x * fq));
+      t[gi] = fmaxf(a0, a1) * (sc[gi].x * fq);
+      mx = fmaxf(mx, t[gi]);
     }
   }
-  return mx;
+  float wx = -INFINITY;
+#pragma unroll
+  for (int gi = 0; gi < 4; ++gi) wx = fmaxf(wx, (t[gi] - mx) + vlog[gi]);  // (NaN where mx is -inf: left out)
+  return make_float2(mx, wx);
 }
 
-// The weights of a row's 64 columns relative to 2^mb, times the value scale and vi, as f16 limbs over the scores (of each
+// The weights of a row's 64 columns relative to 2^mb, times the value scale and wf, as f16 limbs over the scores (of each
 // 16 columns: hi limbs in 0 .. 7, lo limbs in 8 .. 15); returns the sum of the weights proper.
 template <bool FULL>
-__device__ __forceinline__ float weights(uint32_t ts, const float2* scales, float fq, float mb, float vi, int see, uint32_t live) {
+__device__ __forceinline__ float weights(uint32_t ts, const float2* scales, float fq, float mb, float wf, int see, uint32_t live) {
   const uint64_t nmb = pair2(-mb, -mb);
   uint64_t ls = 0;
 #pragma unroll
   for (int gi = 0; gi < 4; ++gi) {
     const float2 sc = scales[gi];
-    const uint64_t f = pair2(sc.x * fq, sc.x * fq), wv = pair2(sc.y * vi, sc.y * vi);
+    const float w = i8_weight_factor(sc.y, wf, kWeightTop);
+    const uint64_t f = pair2(sc.x * fq, sc.x * fq), wv = pair2(w, w);
     const int lim = (live >> gi & 1) ? see - 16 * gi : -1;  // tokens 0 .. lim of the group
     uint32_t v[16], pk[16];
     tmem_ld16(ts + 16 * gi, v);
@@ -353,7 +357,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // where the row's sums gather: four channels of 128 rows side by side, so that a warp's accesses are contiguous
     const size_t block = ((size_t)blockIdx.z * gridDim.y + g) * gridDim.x + blockIdx.x;
     float4* gather = reinterpret_cast<float4*>(ws + L.afrag) + ((block * 2 + u) * 2 + hf) * (H / 4 * 128) + r;
-    float m = -INFINITY, l = 0.f, vref = 0.f;  // reference of the exponents, sum, reference of the value scales
+    // references, in powers of two, of the exponents and, relative to that, of the weights (a page of large values that
+    // hardly weighs does not push the others' weights under f16's range); the sum
+    float m = -INFINITY, wref = -INFINITY, l = 0.f;
     float since = 1.f;                         // what the gathered sums have to be scaled by
     bool have = false;                         // something has been gathered
     int idx = 0;                               // tiles of this unit so far
@@ -393,23 +399,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t there = sh.live[st], live = (there >> (4 * hf)) & 15u;
       const int see = pos - j * KT - 64 * hf;  // columns 0 .. see of the half are visible
       const bool full = __all_sync(0xffffffffu, see >= 63) && live == 15u;
-      // the tile's largest value scale
-      const float vt = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(pow2_above(sh.scale[st][lane & 7].y))));
-      float mx = full ? largest<true>(ts, sh.scale[st] + 4 * hf, fq, see, live) : largest<false>(ts, sh.scale[st] + 4 * hf, fq, see, live);
-      float* box = &sh.mx[idx & 1][u][0][0];
-      box[128 * hf + r] = mx;
+      const float2 top = full ? largest<true>(ts, sh.scale[st] + 4 * hf, sh.vlog[st] + 4 * hf, fq, see, live)
+                              : largest<false>(ts, sh.scale[st] + 4 * hf, sh.vlog[st] + 4 * hf, fq, see, live);
+      float2* box = &sh.mx[idx & 1][u][0][0];
+      box[128 * hf + r] = top;
       asm volatile("bar.sync %0, 256;" ::"r"(1 + u) : "memory");
-      mx = fmaxf(mx, box[128 * (hf ^ 1) + r]);
-      // both halves of a row come to the same reference
-      float factor = 1.f;
+      const float2 its = box[128 * (hf ^ 1) + r];
+      // both halves of a row come to the same references
+      const float mx = fmaxf(top.x, its.x);
       if (mx > m + kSlack) {
-        factor = ex2(m - mx);  // 0 from the first score on
+        l *= ex2(m - mx);  // 0 from the first score on
+        wref -= mx - m;
         m = mx;
-        l *= factor;
       }
-      if (vt > vref) {
-        factor *= vref * pow2_inv(vt);
-        vref = vt;
+      const float mb = m == -INFINITY ? 0.f : m, wx = fmaxf((top.x - mb) + top.y, (its.x - mb) + its.y);
+      float factor = 1.f;
+      if (wx > wref + kSlack) {
+        factor = ex2(wref - wx);
+        wref = wx;
       }
       const bool begin = idx % kRun == 0;
       if (begin ? idx > 0 : __any_sync(0xffffffffu, factor != 1.f)) {
@@ -429,9 +436,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       since *= factor;
-      const float mb = m == -INFINITY ? 0.f : m, vi = vref > 0.f ? pow2_inv(vref) * kWeightTop : 0.f;
-      l += full ? weights<true>(ts, sh.scale[st] + 4 * hf, fq, mb, vi, see, live)
-                : weights<false>(ts, sh.scale[st] + 4 * hf, fq, mb, vi, see, live);
+      const float wf = wref == -INFINITY ? 0.f : i8_two_to(-wref);
+      l += full ? weights<true>(ts, sh.scale[st] + 4 * hf, fq, mb, wf, see, live)
+                : weights<false>(ts, sh.scale[st] + 4 * hf, fq, mb, wf, see, live);
       // infinities and NaN among the window's values lie as zeros in the tile, since zero weights of rows
       // that do not see them would not cancel them: the rows that do see them take them here
       if (there >> GROUPS) {
@@ -466,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     asm volatile("bar.sync %0, 256;" ::"r"(1 + u) : "memory");
     l = sh.l[u][0][r] + sh.l[u][1][r];
     // what is gathered and the last O, in true units, to the output row or to the split's partial sums
-    const float unit = vref * (1.f / kWeightTop), z = direct ? (l == 0.f ? 0.f : unit / l) : unit;
+    const float unit = wref == -INFINITY ? 0.f : ex2(wref) * (1.f / kWeightTop), z = direct ? (l == 0.f ? 0.f : unit / l) : unit;
     float* dst = direct ? out + head * P.dh + H * hf : reinterpret_cast<float*>(ws + L.acc) + (head * SX + sx) * D + H * hf;
     const int width = rr >= rows ? 0 : direct ? min(H, P.dh - H * hf) : H;  // (a multiple of 4; can be negative)
 #pragma unroll 1
@@ -585,6 +592,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           const int at = (j - j0) & 3;
           sh.scale[at][gi] = sc;
+          sh.vlog[at][gi] = __log2f(sc.y);
           sh.bad[at][gi] = bad;
           const uint32_t bits = (uint32_t)(ik[x] >= 0 || (p0 >= nc && p0 < end)) | (bad ? 1u << GROUPS : 0u);
           atomicAnd(&sh.live[at], ~((1u | 1u << GROUPS) << gi));

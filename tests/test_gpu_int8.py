@@ -321,6 +321,55 @@ def test_decode_with_queries_and_scales_far_apart(tq):
     assert torch.equal(out2[0, keep], out[0, keep])
 
 
+def outlier_pages(kind):
+    """(k, v, q) of 12 pages + 4 window tokens, one head, d = 128, whose value scales are far apart: page 3 holds values
+    of 1e18 that weigh nothing (its keys are far from the query), or zeros that take all of the weight, or all of the
+    values are tiny."""
+    g = torch.Generator().manual_seed(70)
+    k, v = torch.randn((1, 196, 1, 128), generator=g) * 0.1, torch.randn((1, 196, 1, 128), generator=g)
+    q = torch.randn((1, 8, 128), generator=g)
+    far = q[0].mean(0) * 40
+    if kind == "huge_but_light":
+        k[0, 48:64, 0] = -far * 10
+        v[0, 48:64] *= 1e18
+    elif kind == "zero_but_heavy":
+        k[0, 48:64, 0] = far * 40
+        v[0, 48:64] = 0
+        v[0, 192:] = 0
+    elif kind == "all_tiny":
+        v *= 1e-36
+        v[0, 192:] = 0
+    return k.cuda(), v.cuda(), q.cuda()
+
+
+@pytest.mark.parametrize("kind", ["huge_but_light", "zero_but_heavy", "all_tiny"])
+@pytest.mark.parametrize("chunk", [1, 5, 20])
+def test_value_scales_far_apart_keep_the_output_precise(tq, kind, chunk):
+    """Against the output itself, not the largest value of the cache: dl <= 2^-12 here (|l| under 2^9 with 2^-21 each
+    way), so 2 dl + 2^-12 of the terms that make up the output."""
+    L = layer(tq, 128, 1, 8, 4)
+    k, v, q = outlier_pages(kind)
+    pc = tq.PagedCache(L, 1, 196)
+    pc.prefill(k, v)
+    qs = q[:, None].repeat(1, chunk, 1, 1).contiguous()
+    out, lse = torch.full(qs.shape, float("nan"), device="cuda"), torch.full(qs.shape[:-1], float("nan"), device="cuda")
+    ws = torch.empty(tq.prefill_workspace_size(L.params, 1, chunk, 196), dtype=torch.uint8, device="cuda")
+    tq.prefill_attention(L.params, pc.cache, chunk, qs, 128**-0.5, out, lse, ws, 196)
+    assert tq.check_device_error() == 0
+    kk, vv = Mirror(L, k, v).values(0, 0, 196, 196)
+    for i in range(chunk):
+        n = 196 - chunk + i + 1
+        for h in range(8):
+            l = 128**-0.5 * kk[:n] @ f64(q)[0, h]
+            p = np.exp(l - l.max())
+            want = p @ vv[:n] / p.sum()
+            terms = (p[:, None] * np.abs(vv[:n])).sum(0).max() / p.sum()
+            got = f64(out)[0, i, h]
+            assert np.isfinite(got).all()
+            # results under 2^-120 may come out as 0
+            assert (np.abs(got - want) <= 2.0**-10 * terms + 2.0**-120).all(), (i, h, np.abs(got - want).max(), terms)
+
+
 def test_decode_flags_bad_state_and_skips_it(tq):
     L = layer(tq, 128, 2, 2, 16)
     T = 100
@@ -387,7 +436,9 @@ def test_decode_static_and_captured_and_on_another_stream(tq):
 @pytest.mark.parametrize("d,head_dim,hkv,g,window,dtype,T,nq", [
     (128, None, 2, 4, 32, "bf16", 200, 64), (128, None, 1, 1, 5, "f32", 1, 1), (128, None, 2, 3, 16, "f16", 150, 150),
     (256, None, 1, 8, 40, "bf16", 130, 33), (128, 80, 2, 5, 8, "f32", 90, 41), (256, 144, 1, 2, 16, "f16", 80, 80),
-    (128, None, 1, 7, 3, "bf16", 530, 129), (128, None, 2, 8, 64, "bf16", 20, 13),
+    (128, None, 1, 7, 3, "bf16", 530, 129), (128, None, 2, 8, 64, "bf16", 20, 13), (128, None, 2, 3, 16, "bf16", 300, 5),
+    (128, None, 1, 1, 20, "f16", 90, 19), (128, None, 2, 2, 40, "f32", 200, 23), (256, None, 2, 1, 16, "bf16", 100, 21),
+    (256, 160, 1, 3, 5, "f32", 77, 11),
 ])
 def test_prefill_attention(tq, d, head_dim, hkv, g, window, dtype, T, nq):
     L = layer(tq, d, hkv, g, window, head_dim)
@@ -418,10 +469,11 @@ def test_prefill_attention(tq, d, head_dim, hkv, g, window, dtype, T, nq):
     assert np.isfinite(oo).all()
 
 
-def test_prefill_attention_of_ragged_sequences(tq):
+@pytest.mark.parametrize("nq", [20, 11])
+def test_prefill_attention_of_ragged_sequences(tq, nq):
     """Sequences of different lengths, one shorter than the chunk (flagged; its first queries see nothing)."""
     L = layer(tq, 128, 2, 4, 16)
-    lens, nq, T = [140, 33, 9], 20, 140
+    lens, T = [140, 33, 9], 140
     k = data((3, T, 2, 128), "bf16", 25)
     pc = tq.PagedCache(L, 3, T)
     for b, n in enumerate(lens):
@@ -460,3 +512,100 @@ def test_chunked_prefill_equals_decode_of_its_last_query(tq):
     qn, kn = f64(q)[0, -1], np.abs(f64(k)).sum(-1).max()
     tol = 2 * (2 * 128**-0.5 * kn * np.abs(qn).max() * 2.0**-18 + 2.0**-16) * float(v.abs().max())
     assert (out[:, -1] - ref).abs().max() <= tol
+
+
+@pytest.mark.parametrize("dtype,nq,g", [("bf16", 60, 4), ("f32", 60, 2), ("bf16", 200, 2), ("bf16", 5, 4)])
+def test_non_finite_window_values_reach_only_the_queries_that_see_them(tq, dtype, nq, g):
+    """A query attends to nothing behind itself, whatever lies there: infinities and NaN among the window's values (and
+    keys) change no query before them, and do reach those after."""
+    L = layer(tq, 128, 2, g, 100)
+    T = 300
+    k, v = data((1, T, 2, 128), dtype, 30), data((1, T, 2, 128), dtype, 31)
+    pc = tq.PagedCache(L, 1, T)
+    pc.prefill(k, v)
+    q = data((1, nq, 2 * g, 128), dtype, 32)
+    ws = torch.empty(tq.prefill_workspace_size(L.params, 1, nq, T), dtype=torch.uint8, device="cuda")
+
+    def run():
+        out = torch.empty(q.shape, device="cuda")
+        tq.prefill_attention(L.params, pc.cache, nq, q, 128**-0.5, out, None, ws, T)
+        return out
+
+    ref = run()
+    at = T - 3  # seen by the last three queries only
+    pc.win_v[0, :, at % 116, 5] = math.inf
+    pc.win_v[0, :, at % 116, 9] = math.nan
+    out = run()
+    assert torch.equal(out[:, :-3], ref[:, :-3])
+    assert not torch.isfinite(out[:, -3:, :, 5]).any() and not torch.isfinite(out[:, -3:, :, 9]).any()
+    keep = [c for c in range(128) if c not in (5, 9)]
+    assert torch.equal(out[:, -3:][..., keep], ref[:, -3:][..., keep])
+    pc.win_k[0, :, at % 116, 7] = math.nan
+    out = run()
+    assert torch.equal(out[:, :-3], ref[:, :-3]) and torch.isnan(out[:, -3:]).all()
+
+
+def test_prefill_attention_skips_pages_that_are_not_there(tq):
+    L = layer(tq, 128, 2, 4, 16)
+    k = data((2, 200, 2, 128), "bf16", 33)
+    pc = tq.PagedCache(L, 2, 200)
+    pc.prefill(k, k)
+    for nq in (40, 3):
+        q = data((2, nq, 8, 128), "bf16", 34)
+        ws = torch.empty(tq.prefill_workspace_size(L.params, 2, nq, 200), dtype=torch.uint8, device="cuda")
+        out = [torch.full(q.shape, float("nan"), device="cuda") for _ in range(2)]
+        tq.prefill_attention(L.params, pc.cache, nq, q, 128**-0.5, out[0], None, ws, 200)
+        table = pc.block_table.clone()
+        pc.block_table[0, 2], pc.block_table[0, 9] = -1, 10**6
+        tq.prefill_attention(L.params, pc.cache, nq, q, 128**-0.5, out[1], None, ws, 200)
+        assert tq.check_device_error() == 0x1
+        assert torch.equal(out[0][1], out[1][1]) and torch.isfinite(out[1]).all()
+        rows = [i for i in range(200) if i // 16 not in (2, 9)]
+        kk, vv = Mirror(L, k, k).values(0, 0, 200, 200)
+        check_attention(f64(q)[0, -1, 0], f64(out[1])[0, -1, 0], O8.attend(f64(q)[0, -1, 0], kk[rows], vv[rows], 128**-0.5)[1],
+                        kk[rows], vv[rows], 128**-0.5, nq)
+        pc.block_table.copy_(table)
+
+
+def test_prefill_attention_captured_and_replayed(tq):
+    L = layer(tq, 128, 2, 8, 16)
+    T, nq = 600, 70
+    k, v = data((1, T, 2, 128), "bf16", 35), data((1, T, 2, 128), "bf16", 36)
+    pc = tq.PagedCache(L, 1, T)
+    pc.prefill(k, v)
+    q = data((1, nq, 16, 128), "bf16", 37)
+    ws = torch.empty(tq.prefill_workspace_size(L.params, 1, nq, T), dtype=torch.uint8, device="cuda")
+    ref, out = torch.empty(q.shape, device="cuda"), torch.empty(q.shape, device="cuda")
+    tq.prefill_attention(L.params, pc.cache, nq, q, 128**-0.5, ref, None, ws, T)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        tq.prefill_attention(L.params, pc.cache, nq, q, 128**-0.5, out, None, ws, T)
+    ws.fill_(0xFF)  # the workspace holds nothing from call to call
+    graph.replay()
+    assert torch.equal(out, ref)
+    q.mul_(0.5)
+    graph.replay()
+    tq.prefill_attention(L.params, pc.cache, nq, q, 128**-0.5, ref, None, ws, T)
+    assert torch.equal(out, ref) and tq.check_device_error() == 0
+
+
+@pytest.mark.parametrize("scale", [-0.05, 0.0])
+def test_scales_below_and_at_zero(tq, scale):
+    L = layer(tq, 128, 1, 4, 16)
+    T = 300
+    k, v = data((1, T, 1, 128), "bf16", 38), data((1, T, 1, 128), "bf16", 39)
+    pc = tq.PagedCache(L, 1, T)
+    pc.prefill(k, v)
+    kk, vv = Mirror(L, k, v).values(0, 0, T, T)
+    for nq in (30, 2):
+        q = data((1, nq, 4, 128), "bf16", 40)
+        ws = torch.empty(tq.prefill_workspace_size(L.params, 1, nq, T), dtype=torch.uint8, device="cuda")
+        out, lse = torch.empty(q.shape, device="cuda"), torch.empty(q.shape[:-1], device="cuda")
+        tq.prefill_attention(L.params, pc.cache, nq, q, scale, out, lse, ws, T)
+        for i in (0, nq - 1):
+            n = T - nq + i + 1
+            for h in range(4):
+                o, z, _ = O8.attend(f64(q)[0, i, h], kk[:n], vv[:n], scale)
+                dl = abs(scale) * (np.abs(kk).sum(1) * np.abs(f64(q)[0, i, h]).max()).max() * 2.0**-18
+                assert np.abs(f64(out)[0, i, h] - o).max() <= (2 * dl + 2.0**-16) * np.abs(vv).max()
+                assert abs(float(lse[0, i, h]) - z) <= dl + 2.0**-18 * max(1, abs(z))
