@@ -7,18 +7,26 @@
 // by a power of two a row) or two limbs (float), and the weights P vs are two limbs, since one f16 limb would
 // leave 2^-12 of the float output: a tile costs one product for S (two for float queries) and two for O.
 //
-//   warps 0-7, 8-15  a unit each, two threads a row: each takes its half of the S row from tensor memory
-//                    (tcgen05.ld), the halves agree on the reference of the exponents, and write P's limbs over S.
+//   warps 0-7, 8-15  a unit (row tile) each, two threads a row: each takes its half of the S row from tensor memory
+//                    (tcgen05.ld), the halves agree on the references of the exponents, and write P's limbs over S.
 //                    The references follow the running maxima only when those have grown by 2^8, so O stays as it is in
-//                    almost every tile.  O is added to memory (scratch, in L2) and begun anew every four
-//                    tiles: the tensor cores' accumulation truncates, 2^-25 of O a step; over the whole of a long
-//                    context that would be 1e-5, over four tiles it is under 1e-6.  (O in registers instead, added
-//                    after every tile, needs 130 a thread, 96 are there: its spills went to L2 and the chunk of
-//                    2048 queries over 16384 tokens took 1283 us.)
-//   warps 16-19      turn the tile's codes (and the float16 window rows) into f16 operands in shared memory.
+//                    almost every tile.  O is added to memory (scratch, in L2) and begun anew every eight tiles: the
+//                    tensor cores' accumulation truncates, 2^-25 of O a step, which over the whole of a long context
+//                    would pass 1e-5 of the float output; so it stays at 1.7e-6 over 16384 tokens (the plain float
+//                    form: 2.4e-6; begun anew every four tiles: 1e-6, but 60 us more of 930).
+//   warps 16-19      turn the tile's codes (and the float16 window rows) into f16 operands in shared memory: keys two
+//                    tiles ahead, values when the products that read the last ones have ended; the pages come as they
+//                    are by bulk copies.  The operands' strides are padded so that these stores meet no bank twice
+//                    (tcgen05.mma reads them as fast: 64.5 cycles a 128 x 128 x 16 either way).
 //   warp 20          one thread issues tcgen05.mma; S_u of the next tile runs while the other unit is in its softmax.
 // With one row tile (RT = 1: up to 128 rows, or float queries, whose second limb takes the second tile's
 // shared memory) the units take the key tiles in turn, as two splits that the joining kernel adds up.
+//
+// What bounds it: a tile of 256 rows x 128 tokens takes about 6800 cycles, 3100 of them products.  A unit's softmax takes
+// 4000 (of 16 warps' 13700 instructions an SM issues 1.7 a cycle), then it waits for its own O and next S: the two units
+// cover about half of each other's.  Measured on the way, on the chunk of 2048 queries over 16384 tokens, 32 heads: O in
+// registers after every tile 1283 us (130 registers a thread where 96 are there: the spills go to L2); half tiles of 64
+// tokens, with S of one half during the softmax of the other, 1210 us (every step's waits twice); now 930 us.
 #include <math.h>
 
 #include <algorithm>
@@ -364,9 +372,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool have = false;                         // something has been gathered
     int idx = 0;                               // tiles of this unit so far
     bool failed = false;
-    // gathered = gathered * since + O
+    // gathered = gathered * since + O (one thread owns the place: no atomics, and the additions' order is the tiles'; as
+    // reductions without reading back they cost 37 us more on the chunk of 2048 queries over 16384 tokens)
     auto gather_o = [&]() {
-      const bool scaled = __any_sync(0xffffffffu, since != 1.f);
 #pragma unroll 1
       for (int c = 0; c < H / 16; ++c) {
         uint32_t v[16];
@@ -374,18 +382,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float4* at = gather + (4 * c + i) * 128;
-          float4 x = make_float4(__uint_as_float(v[4 * i]), __uint_as_float(v[4 * i + 1]), __uint_as_float(v[4 * i + 2]),
-                                 __uint_as_float(v[4 * i + 3]));
-          if (have && !scaled) {
-            // (one thread owns the place: the additions' order is the tiles' order)
-            asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(at), "f"(x.x), "f"(x.y), "f"(x.z), "f"(x.w) : "memory");
-            continue;
-          }
-          if (have) {
-            const float4 a = __ldcg(at);
-            x = make_float4(fmaf(a.x, since, x.x), fmaf(a.y, since, x.y), fmaf(a.z, since, x.z), fmaf(a.w, since, x.w));
-          }
-          __stcg(at, x);
+          float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (have) a = __ldcg(at);
+          __stcg(at, make_float4(fmaf(a.x, since, __uint_as_float(v[4 * i])), fmaf(a.y, since, __uint_as_float(v[4 * i + 1])),
+                                 fmaf(a.z, since, __uint_as_float(v[4 * i + 2])), fmaf(a.w, since, __uint_as_float(v[4 * i + 3]))));
         }
       }
       have = true;
@@ -812,7 +812,8 @@ static size_t places(const KParams& P, int batch, int n_query, int splits, bool 
 }
 
 // Splits of the key tiles: blocks are one to an SM, so the count whose last wave is fullest, at least four tiles
-// a split; the joining costs a pass over the partial outputs (about 3 % of a block's work a split).
+// a split.  A split costs about 6.5 % of a block's work (its start, and a pass over its partial outputs): the chunk of 2048
+// queries over 16384 tokens, 256 blocks of two row tiles, takes 930 us whole (1.7 waves), 959 us in four splits (6.7).
 WsLayout int8_prefill_layout(const KParams& P, int batch, int n_query, int max_ctx, int num_sms) {
   const long long rt = ((long long)n_query * P.G + 255) / 256, units = std::max(1LL, rt * batch * P.hkv);
   const int tiles = std::max(1, (max_ctx + KT - 1) / KT);
@@ -822,7 +823,7 @@ WsLayout int8_prefill_layout(const KParams& P, int batch, int n_query, int max_c
     if (S > 1 && tiles / S < 4) break;
     if (units * S > 65535) break;
     const double w = (double)(units * S) / std::max(1, num_sms);
-    const double eff = w / ceil(w) / (1.0 + 0.03 * (S - 1));
+    const double eff = w / ceil(w) / (1.0 + 0.065 * (S - 1));
     if (eff > best_eff + 1e-9) {
       best_eff = eff;
       best = S;
