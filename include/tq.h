@@ -16,6 +16,9 @@
  *   - Device pointers are marked [device]; host pointers [host].
  *   - Asynchrony: calls that take a cudaStream_t only enqueue work on that
  *     stream and never synchronise, except tq_check_device_error.
+ *     (Kernels of the 8-bit arm and of the page calls get their shared-memory
+ *     allowance once a process and device: after cudaDeviceReset they return
+ *     TQ_ERR_CUDA.)
  *   - Errors: arguments are checked on the host before any launch; a failed
  *     check returns a tq_status != TQ_OK, launches nothing, and sets a
  *     thread-local message readable with tq_last_error().  A launch failure

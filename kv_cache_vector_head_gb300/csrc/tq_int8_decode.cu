@@ -3,9 +3,9 @@
 //   l_t = scale ks <q, c_t> (pages), scale <q, k_t> (float16 window);  out = sum_t p_t vs cv_t / sum_t p_t.
 //
 // The G <= 8 query heads of a KV head share every load; of a chunk of queries (prefill attention where the tcgen05
-// kernel does not apply) so do the heads of 8 / G queries, each row with its own causal length.  Both products run on mma.m16n8k16 with
-// operands exact in f16: the codes as they are (integers up to 127), the query and the softmax weights
-// as f16 hi + lo limbs in rows h and h + 8 of the 16-row tile (22 bits; a single f16 limb would leave
+// kernel does not apply) so do the heads of 8 / G queries, each row with its own causal length.  Both products run
+// on mma.m16n8k16 with operands exact in f16: the codes as they are (integers up to 127), the query and the softmax
+// weights as f16 hi + lo limbs in rows h and h + 8 of the 16-row tile (22 bits; a single f16 limb would leave
 // 2^-12 of the float output, and with G <= 8 the second limb fills rows that were empty).  A query row is
 // scaled by a power of two so that its limbs keep clear of f16's subnormals; the pages' value scales ride on the
 // weights, which have a reference of their own, the largest p vs so far (the exponents' is the largest p): a page of
@@ -15,6 +15,13 @@
 // of the first product in the layout the second one takes them: a warp carries a page from its codes to the
 // accumulators without another warp.  Warps take the pages (16 tokens; the window in groups of 16) of their
 // split in turn, each through its own ring of bulk copies, and meet once at the end.
+//
+// What bounds it: 2 x 16 d + 8 bytes a page and head.  32 sequences of up to 8192 tokens, 8 heads, d = 128 (407 MB): 88 us,
+// 4.6 TB/s, of which the copies with everything but the products and the softmax take 80 (the same copies alone reach
+// 6.6 TB/s: the rest is the blocks' start, the last wave and the joining); one of 262144 tokens: 105 us, 5.1 TB/s.
+// Two pages an iteration (101 us), keys as subnormal f16 bytes with a bias (no faster, three times the error), the splits
+// of a unit as a cluster that joins in shared memory (100 us, and no faster at 517 tokens), two blocks with half of the
+// value channels each at d = 256 (114 against 99 us, 32 x 8192 tokens, 4 heads) were measured and left out.
 #include <math.h>
 
 #include <algorithm>
@@ -35,7 +42,7 @@ constexpr float kWeightTop = 16384.f;  // f16 weights reach up to this: lo limbs
 
 __host__ __device__ constexpr int ctas_per_sm(int d) { return d == 128 ? 4 : 2; }
 __host__ __device__ constexpr int raw_bytes(int d) { return 32 * d + kI8Head; }  // a page's scales and codes
-constexpr int kRing = 3;  // pages in flight a warp
+constexpr int kRing = 3;  // pages in flight a warp (two or four are no faster)
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
@@ -524,7 +531,8 @@ cudaError_t decode(const KParams& P, const KCache& C, const void* q, int dtype, 
 // unit four splits or more (one sequence of 262144 tokens, 8 heads: 76 splits 114 us, two waves 126 us); else two
 // waves, since few splits of unequal sequences leave a long tail (32 x 8192 tokens, 8 heads: 2 or 3 splits 103 us, 5
 // splits 93 us).  A split keeps a group for each of its warps.  (Blocks that share all sequences' groups evenly in
-// one wave were no faster, 95 us, and would make a sequence's rounding depend on the others in its batch.)
+// one wave were no faster, 95 us, and would make a sequence's rounding depend on the others in its batch.)  A warp adds up
+// at most 64 groups: the tensor cores' accumulation truncates, 4e-6 of the output over 256 groups.
 WsLayout int8_ws_layout(const KParams& P, int batch, int n_query, long long max_items, int n_splits, int num_sms) {
   WsLayout L{};
   long long S = n_splits;
@@ -534,6 +542,7 @@ WsLayout int8_ws_layout(const KParams& P, int batch, int n_query, long long max_
     S = slots / units;
     if (S < 4) S = (2 * slots + units - 1) / units;
     S = std::min(S, (max_items + kWarps - 1) / kWarps);
+    S = std::max(S, (max_items + 64 * kWarps - 1) / (64 * kWarps));
   }
   S = std::max(1LL, std::min(S, std::min(max_items, 65535LL)));
   L.n_comp_splits = (int)S;

@@ -10,10 +10,11 @@
 //   warps 0-7, 8-15  a unit (row tile) each, two threads a row: each takes its half of the S row from tensor memory
 //                    (tcgen05.ld), the halves agree on the references of the exponents, and write P's limbs over S.
 //                    The references follow the running maxima only when those have grown by 2^8, so O stays as it is in
-//                    almost every tile.  O is added to memory (scratch, in L2) and begun anew every eight tiles: the
+//                    almost every tile.  O is added to memory (scratch, in L2) and begun anew every four tiles: the
 //                    tensor cores' accumulation truncates, 2^-25 of O a step, which over the whole of a long context
-//                    would pass 1e-5 of the float output; so it stays at 1.7e-6 over 16384 tokens (the plain float
-//                    form: 2.4e-6; begun anew every four tiles: 1e-6, but 60 us more of 930).
+//                    would pass 1e-5 of the float output; so it stays at 1e-6 over 16384 tokens (the plain float
+//                    form: 2.4e-6; begun anew every eight tiles 1.7e-6, which at 2500 tokens is 1.7 times the plain
+//                    form's error, and 6 % faster).
 //   warps 16-19      turn the tile's codes (and the float16 window rows) into f16 operands in shared memory: keys two
 //                    tiles ahead, values when the products that read the last ones have ended; the pages come as they
 //                    are by bulk copies.  The operands' strides are padded so that these stores meet no bank twice
@@ -26,7 +27,7 @@
 // 4000 (of 16 warps' 13700 instructions an SM issues 1.7 a cycle), then it waits for its own O and next S: the two units
 // cover about half of each other's.  Measured on the way, on the chunk of 2048 queries over 16384 tokens, 32 heads: O in
 // registers after every tile 1283 us (130 registers a thread where 96 are there: the spills go to L2); half tiles of 64
-// tokens, with S of one half during the softmax of the other, 1210 us (every step's waits twice); now 930 us.
+// tokens, with S of one half during the softmax of the other, 1210 us (every step's waits twice); now 990 us.
 #include <math.h>
 
 #include <algorithm>
@@ -49,7 +50,7 @@ constexpr int kThreads = 32 * (kSoftWarps + kConvWarps + 1);
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kWeightTop = 64.f;   // weights reach 2^8 above it: 2^14 in f16
 constexpr float kSlack = 8.f;          // log2 of how far a score may pass the reference
-constexpr int kRun = 8;                // tiles that O gathers in tensor memory
+constexpr int kRun = 4;                // tiles that O gathers in tensor memory
 
 // Shared-memory operands without swizzle: core matrices of 8 rows x 16 bytes; LBO steps along the contraction
 // (8 elements), SBO along the rows (8).
@@ -813,7 +814,7 @@ static size_t places(const KParams& P, int batch, int n_query, int splits, bool 
 
 // Splits of the key tiles: blocks are one to an SM, so the count whose last wave is fullest, at least four tiles
 // a split.  A split costs about 6.5 % of a block's work (its start, and a pass over its partial outputs): the chunk of 2048
-// queries over 16384 tokens, 256 blocks of two row tiles, takes 930 us whole (1.7 waves), 959 us in four splits (6.7).
+// queries over 16384 tokens, 256 blocks of two row tiles, takes 930 us whole (1.7 waves), 959 us in four splits (6.7; both with O begun anew every eight tiles).
 WsLayout int8_prefill_layout(const KParams& P, int batch, int n_query, int max_ctx, int num_sms) {
   const long long rt = ((long long)n_query * P.G + 255) / 256, units = std::max(1LL, rt * batch * P.hkv);
   const int tiles = std::max(1, (max_ctx + KT - 1) / KT);
