@@ -498,7 +498,9 @@ tq_status tq_track_pages(const tq_layer_params* p, const tq_cache* cache, const 
  * with at most `budget` full pages keeps its state.  With e pages dropped:
  *   block table   kept pages in their order, then a partly filled page (window ==
  *                 0), then the dropped pages in theirs (the sequence fills them
- *                 again first), then the other entries unchanged
+ *                 again first), then the other entries unchanged.  A page
+ *                 that another table or sequence still reads must not be left to be
+ *                 filled again: the caller takes it out of this table
  *   counters      seq_len and n_compressed fall by 16 e
  *   window        row of position p moves to the slot of p - 16 e
  *   mass_after    the kept pages' masses in their order (and the partly filled

@@ -480,12 +480,17 @@ cudaError_t allow_dynamic_smem(const void* kern, size_t bytes) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  std::lock_guard<std::mutex> lk(mu);
-  size_t& have = given[{kern, dev}];
-  if (bytes <= have || bytes <= 40 * 1024) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess) have = bytes;
-  return e;
+  if (bytes <= 40 * 1024) return cudaSuccess;
+  try {
+    std::lock_guard<std::mutex> lk(mu);
+    size_t& have = given[{kern, dev}];
+    if (bytes <= have) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess) have = bytes;
+    return e;
+  } catch (...) {  // (no memory for an entry: nothing crosses the C entry)
+    return cudaErrorMemoryAllocation;
+  }
 }
 
 cudaError_t read_clear_int8_error(unsigned* bits) {
