@@ -1,4 +1,5 @@
 // C ABI entry points of libtq: argument checks on the host, then launches.
+#include <climits>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -214,6 +215,9 @@ static tq_status make_cache(const tq_cache* c, const KParams& K, KCache* C, bool
   return TQ_OK;
 }
 
+// Positions that the 8-bit arm and the page calls take: a bound rounded up to a tile stays within 32 bits.
+static bool ctx_ok(int max_ctx) { return max_ctx >= 0 && max_ctx <= INT_MAX - 1023; }
+
 // Decode workspace of either kind of layer (8-bit arm: pages and window in groups of 16 tokens).
 static WsLayout decode_layout(const KParams& K, int batch, int max_ctx, int n_splits) {
   if (K.int8) return int8_ws_layout(K, batch, 1, (long long)(max_ctx + TQ_PAGE_SIZE - 1) / TQ_PAGE_SIZE + 1, n_splits, num_sms());
@@ -341,6 +345,10 @@ extern "C" size_t tq_decode_workspace_size(const tq_layer_params* p, int batch, 
   KParams K;
   if (make_params(p, &K, false) != TQ_OK || batch < 1 || max_ctx < 0 || n_splits < 0) return 0;
   if (!decode_rows_ok(K, batch)) return 0;
+  if (K.int8 && !ctx_ok(max_ctx)) {
+    set_error("max_ctx must be <= 2^31 - 1024");
+    return 0;
+  }
   clear_error();
   return decode_layout(K, batch, max_ctx, n_splits).total;
 }
@@ -359,6 +367,7 @@ extern "C" tq_status tq_decode_attention(const tq_layer_params* p, const tq_cach
   if (max_ctx < 0 || n_splits < 0) return fail(TQ_ERR_INVALID_ARG, "max_ctx and n_splits must be >= 0");
   if (!(scale == scale)) return fail(TQ_ERR_INVALID_ARG, "scale is NaN");
   if (K.int8 && !aligned(out, 16)) return fail(TQ_ERR_INVALID_ARG, "int8: out must be 16-byte aligned");
+  if (K.int8 && !ctx_ok(max_ctx)) return fail(TQ_ERR_INVALID_ARG, "max_ctx must be <= 2^31 - 1024");
   if (!decode_rows_ok(K, cache->batch)) return fail(TQ_ERR_INVALID_ARG, "batch must be <= 65535 and batch * G <= 262140");
   const WsLayout L = decode_layout(K, cache->batch, max_ctx, n_splits);
   if (workspace_bytes < L.total) {
@@ -378,6 +387,10 @@ extern "C" size_t tq_prefill_workspace_size(const tq_layer_params* p, int batch,
   KParams K;
   if (make_params(p, &K, false) != TQ_OK || batch < 1 || n_query < 1 || max_ctx < 0) return 0;
   if (!decode_rows_ok(K, (long long)batch * n_query)) return 0;
+  if (K.int8 && !ctx_ok(max_ctx)) {
+    set_error("max_ctx must be <= 2^31 - 1024");
+    return 0;
+  }
   clear_error();
   WsLayout L;
   return prefill_layout(K, batch, n_query, max_ctx, &L);
@@ -399,6 +412,7 @@ extern "C" tq_status tq_prefill_attention(const tq_layer_params* p, const tq_cac
   if (max_ctx < 0) return fail(TQ_ERR_INVALID_ARG, "max_ctx must be >= 0");
   if (!(scale == scale)) return fail(TQ_ERR_INVALID_ARG, "scale is NaN");
   if (K.int8 && !aligned(out, 16)) return fail(TQ_ERR_INVALID_ARG, "int8: out must be 16-byte aligned");
+  if (K.int8 && !ctx_ok(max_ctx)) return fail(TQ_ERR_INVALID_ARG, "max_ctx must be <= 2^31 - 1024");
   WsLayout L;
   const size_t need = prefill_layout(K, cache->batch, n_query, max_ctx, &L);
   if (workspace_bytes < need) {
@@ -483,8 +497,8 @@ static tq_status check_choice(int k, int n_sink, int n_recent, const char* what)
 extern "C" size_t tq_select_workspace_size(const tq_layer_params* p, int batch, int max_ctx) {
   KParams K;
   if (make_params(p, &K, false) != TQ_OK) return 0;
-  if (!K.int8 || batch < 1 || batch > 65535 || max_ctx < 0) {
-    set_error("tq_select_workspace_size: an int8 layer, batch 1..65535 and max_ctx >= 0");
+  if (!K.int8 || batch < 1 || batch > 65535 || !ctx_ok(max_ctx)) {
+    set_error("tq_select_workspace_size: an int8 layer, batch 1..65535 and 0 <= max_ctx <= 2^31 - 1024");
     return 0;
   }
   clear_error();
@@ -504,7 +518,7 @@ extern "C" tq_status tq_select_pages(const tq_layer_params* p, const tq_cache* c
   if ((s = check_choice(n_sel, n_sink, n_recent, "tq_select_pages")) != TQ_OK) return s;
   if (!q || !pages || !counts || !workspace) return fail(TQ_ERR_INVALID_ARG, "null q / pages / counts / workspace");
   if (!aligned(workspace, 256)) return fail(TQ_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
-  if (max_ctx < 0) return fail(TQ_ERR_INVALID_ARG, "max_ctx must be >= 0");
+  if (!ctx_ok(max_ctx)) return fail(TQ_ERR_INVALID_ARG, "max_ctx must be 0 .. 2^31 - 1024");
   if (!decode_rows_ok(K, cache->batch)) return fail(TQ_ERR_INVALID_ARG, "batch must be <= 65535 and batch * G <= 262140");
   if (workspace_bytes < select_ws_bytes(K, cache->batch, max_ctx)) {
     set_error("workspace too small: %zu < %zu", workspace_bytes, select_ws_bytes(K, cache->batch, max_ctx));
@@ -516,7 +530,7 @@ extern "C" tq_status tq_select_pages(const tq_layer_params* p, const tq_cache* c
 }
 
 static WsLayout pages_layout(const KParams& K, int batch, int n_sel, int n_splits) {
-  return int8_ws_layout(K, batch, 1, (long long)n_sel + (K.window + 2 * TQ_PAGE_SIZE - 2) / TQ_PAGE_SIZE, n_splits, num_sms());
+  return int8_ws_layout(K, batch, 1, (long long)n_sel + ((long long)K.window + 2 * TQ_PAGE_SIZE - 2) / TQ_PAGE_SIZE, n_splits, num_sms());
 }
 
 extern "C" size_t tq_decode_pages_workspace_size(const tq_layer_params* p, int batch, int n_sel, int n_splits) {
@@ -547,6 +561,7 @@ extern "C" tq_status tq_decode_attention_pages(const tq_layer_params* p, const t
   if (max_ctx < 0 || n_splits < 0 || n_sel < 1) return fail(TQ_ERR_INVALID_ARG, "max_ctx, n_splits >= 0 and n_sel >= 1");
   if (!(scale == scale)) return fail(TQ_ERR_INVALID_ARG, "scale is NaN");
   if (K.int8 && !aligned(out, 16)) return fail(TQ_ERR_INVALID_ARG, "int8: out must be 16-byte aligned");
+  if (K.int8 && !ctx_ok(max_ctx)) return fail(TQ_ERR_INVALID_ARG, "max_ctx must be <= 2^31 - 1024");
   if (!decode_rows_ok(K, cache->batch)) return fail(TQ_ERR_INVALID_ARG, "batch must be <= 65535 and batch * G <= 262140");
   const WsLayout L = pages_layout(K, cache->batch, n_sel, n_splits);
   if (workspace_bytes < L.total) {
@@ -568,7 +583,8 @@ extern "C" tq_status tq_track_pages(const tq_layer_params* p, const tq_cache* ca
   if (s != TQ_OK) return s;
   if ((s = make_cache(cache, K, &C, false)) != TQ_OK) return s;
   if (!scores || !lse || !mass) return fail(TQ_ERR_INVALID_ARG, "null scores / lse / mass");
-  if (max_ctx < 0 || cache->batch > 65535) return fail(TQ_ERR_INVALID_ARG, "max_ctx >= 0 and batch <= 65535");
+  if (!ctx_ok(max_ctx) || cache->batch > 65535)
+    return fail(TQ_ERR_INVALID_ARG, "max_ctx must be 0 .. 2^31 - 1024 and batch <= 65535");
   if (max_ctx == 0) return ok();
   return cuda_status(launch_track(K, C, scores, lse, mass, max_ctx, reinterpret_cast<cudaStream_t>(stream)), "tq_track_pages");
 }
@@ -651,6 +667,7 @@ extern "C" tq_status tq_decode_attention_static(const tq_layer_params* p, const 
   if (!cache || cache->batch < 1 || max_ctx < 0 || n_splits < 0)
     return fail(TQ_ERR_INVALID_ARG, "tq_decode_attention_static: bad cache, max_ctx or n_splits");
   if (!decode_rows_ok(K, cache->batch)) return fail(TQ_ERR_INVALID_ARG, "batch must be <= 65535 and batch * G <= 262140");
+  if (K.int8 && !ctx_ok(max_ctx)) return fail(TQ_ERR_INVALID_ARG, "max_ctx must be <= 2^31 - 1024");
   const size_t need = decode_layout(K, cache->batch, max_ctx, n_splits).total;
   if (need > (size_t)TQ_STATIC_SCRATCH_BYTES) {
     set_error("tq_decode_attention_static: this configuration needs %zu bytes of scratch, more than the %u-byte "

@@ -280,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     nc = min(max(nc, 0), n) / kPage * kPage;
     if (nc / kPage > C.max_pages || n - nc >= C.ring) {
       wrong = true;
-      nc = min(nc, C.max_pages * kPage);
+      nc = (int)min((long long)nc, (long long)C.max_pages * kPage);
       n = min(n, nc + C.ring - 1);
     }
     if (wrong && tid == 0) atomicOr(&g_int8_prefill_err, TQ_DEVERR_SEQ_LEN);

@@ -299,6 +299,9 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const __grid_co
 
 constexpr int kTrackWarps = 8;
 
+// Pages that `tokens` >= 0 tokens take.  Counters may hold anything: the rounding up must not pass 32 bits.
+__device__ __forceinline__ int pages_of(int tokens) { return tokens / kPage + (tokens % kPage ? 1 : 0); }
+
 // One block eight pages (128 tokens, four lanes of four tokens a page), its warps take the heads in turn.
 template <bool VEC>
 __global__ void __launch_bounds__(32 * kTrackWarps) track_kernel(const __grid_constant__ KCache C, int hq,
@@ -308,7 +311,7 @@ __global__ void __launch_bounds__(32 * kTrackWarps) track_kernel(const __grid_co
   const int b = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = C.seq_len[b];
   int nc = C.n_compressed[b];
-  if (n < 0 || n > max_ctx || nc < 0 || nc > n || (nc + kPage - 1) / kPage > C.max_pages) {
+  if (n < 0 || n > max_ctx || nc < 0 || nc > n || pages_of(nc) > C.max_pages) {
     if (threadIdx.x == 0 && blockIdx.x == 0) atomicOr(&g_pages_err, TQ_DEVERR_SEQ_LEN);
     return;
   }
@@ -352,7 +355,7 @@ __global__ void __launch_bounds__(32 * kTrackWarps) track_kernel(const __grid_co
 // Pages dropped from a sequence, -1 where its counters are no valid state.
 __device__ __forceinline__ int dropped(const KCache& C, int b, int budget) {
   const int n = C.seq_len[b], nc = C.n_compressed[b];
-  if (nc < 0 || n < nc || (nc + kPage - 1) / kPage > C.max_pages) return -1;
+  if (nc < 0 || n < nc || pages_of(nc) > C.max_pages || n - nc > C.ring) return -1;
   return max(0, nc / kPage - budget);
 }
 
@@ -417,7 +420,7 @@ __global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_c
   if (list)
     for (int i = keep + threadIdx.x; i < budget; i += kPickThreads) list[i] = -1;
   if (e <= 0) {  // nothing goes: the state as it is
-    const int held = e < 0 ? mp : (nc + kPage - 1) / kPage;
+    const int held = e < 0 ? mp : pages_of(nc);
     for (int i = threadIdx.x; i < mp; i += kPickThreads) {
       const int32_t page = table[i];
       const float x = m[i];

@@ -242,6 +242,30 @@ def test_eviction_of_a_bad_state_changes_nothing(tq):
     assert torch.equal(pc.block_table[1:], old[0][1:]) and torch.equal(mass[1:], old[1][1:])
 
 
+def test_counters_that_hold_anything_are_flagged(tq):
+    big = 2**31 - 1
+    L = layer(tq, 128, 1, 2, 16)
+    states = [(160, 144), (big, big), (big, big - 15), (big, 144), (-1, -1), (160, -16), (-2**31, 0)]
+    pc = tq.PagedCache(L, len(states), 160, pool_pages=10)
+    pc.seq_len.copy_(torch.tensor([s[0] for s in states]))
+    pc.n_compressed.copy_(torch.tensor([s[1] for s in states]))
+    mass = torch.rand((len(states), 10), device="cuda")
+    old = (pc.block_table.clone(), mass.clone())
+    scores, lse = torch.zeros((len(states), 2, 160), device="cuda"), torch.zeros((len(states), 2), device="cuda")
+    tq.track_pages(L.params, pc.cache, scores, lse, mass, 160)
+    assert tq.check_device_error() == 0x2
+    assert torch.equal(mass[1:], old[1][1:]) and not torch.equal(mass[0], old[1][0])
+    q = data((len(states), 2, 128), "f32", 50)
+    pages, counts = torch.empty((len(states), 1, 4), dtype=torch.int32, device="cuda"), torch.empty((len(states), 1), dtype=torch.int32, device="cuda")
+    ws = torch.empty(tq.select_workspace_size(L.params, len(states), 160), dtype=torch.uint8, device="cuda")
+    tq.select_pages(L.params, pc.cache, q, 4, 1, 1, pages, counts, ws, 160)
+    assert tq.check_device_error() == 0x2 and counts.flatten().tolist() == [4] + [0] * (len(states) - 1)
+    kept = evict(tq, pc, mass, 4, 0, 0)
+    assert tq.check_device_error() == 0x2
+    assert [tuple(s) for s in zip(pc.seq_len.tolist(), pc.n_compressed.tolist())] == [(80, 64)] + states[1:]
+    assert torch.equal(pc.block_table[1:], old[0][1:]) and torch.equal(mass[1:], old[1][1:]) and (kept[1:] == -1).all()
+
+
 def test_a_thinned_turboquant_cache_attends_to_what_is_left(tq):
     """Eviction moves pages of any arm: 3-bit keys without a window, the last page partly filled.  The thinned cache's
     decode equals that of a cache that was given the kept tokens only (equal records: the same bits)."""

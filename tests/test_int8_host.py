@@ -136,6 +136,24 @@ def test_refusals_of_the_calls(L):
     assert ev(P=ctypes.byref(params(L, window=12785))) == unsup
 
 
+def test_bounds_that_round_up_past_32_bits_are_refused(L):
+    p, c = params(L), fake_cache(L)
+    P, C = ctypes.byref(p), ctypes.byref(c)
+    big, bad = 1 << 60, L.TQ_ERR_INVALID_ARG
+    lib = L.lib()
+    for ctx in (2**31 - 1, 2**31 - 1023):
+        assert lib.tq_decode_workspace_size(P, 1, ctx, 1) == 0
+        assert lib.tq_prefill_workspace_size(P, 1, 1, ctx) == 0
+        assert lib.tq_select_workspace_size(P, 1, ctx) == 0
+        assert call(L, "tq_decode_attention", P, C, 4096, 1, 0.1, 4096, None, None, 4096, big, ctx, 0, None) == bad
+        assert call(L, "tq_decode_attention_static", P, C, 4096, 1, 0.1, 4096, None, None, ctx, 1, None) == bad
+        assert call(L, "tq_prefill_attention", P, C, 1, 4096, 1, 0.1, 4096, None, 4096, big, ctx, None) == bad
+        assert call(L, "tq_select_pages", P, C, 4096, 1, 8, 1, 1, 4096, 4096, 4096, big, ctx, None) == bad
+        assert call(L, "tq_decode_attention_pages", P, C, 4096, 1, 0.1, 4096, 4096, 8, 4096, None, 4096, big, ctx, 0, None) == bad
+        assert call(L, "tq_track_pages", P, C, 4096, 4096, 4096, ctx, None) == bad
+    assert lib.tq_decode_workspace_size(P, 1, 2**31 - 1024, 1) > 0 and lib.tq_select_workspace_size(P, 1, 2**31 - 1024) > 0
+
+
 def test_a_layer_is_made_without_a_gpu_only_parameters(L):
     import kv_cache_vector_head_gb300 as tq
 
