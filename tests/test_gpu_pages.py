@@ -360,3 +360,88 @@ def test_a_run_of_them_together(tq):
             n, nc = n - e, nc - e
             assert pc.seq_len.tolist() == [n] * 2 and pc.n_compressed.tolist() == [nc] * 2
     assert tq.check_device_error() == 0
+
+
+def test_pages_behind_4_gb_of_the_pool(tq):
+    """The same sequence in the pool's first and in its last pages (byte offsets past 32 bits): equal bits everywhere."""
+    L = layer(tq, 128, 1, 4, 16)
+    T, far = 400, 1000100
+    assert (far - 64) * L.sub_bytes > 2**32
+    low = tq.PagedCache(L, 1, T + 16, pool_pages=far)
+    high = tq.PagedCache(L, 1, T + 16, pool_pages=1)
+    high.share_pages(low)
+    high.block_table.copy_(far - 1 - torch.arange(high.max_pages, dtype=torch.int32)[None])
+    k, v = data((1, T + 16, 1, 128), "bf16", 60), data((1, T + 16, 1, 128), "bf16", 61)
+    got = []
+    for pc in (low, high):
+        pc.prefill(k[:, :T], v[:, :T])
+        for t in range(T, T + 16):
+            pc.append(k[:, t].contiguous(), v[:, t].contiguous())
+        n = T + 16
+        rk, rv = torch.zeros((1, n, 1, 128), device="cuda"), torch.zeros((1, n, 1, 128), device="cuda")
+        tq.read_cache(L.params, pc.cache, rk, rv, 0, n)
+        q = data((1, 4, 128), "bf16", 62)
+        out, lse, _ = decode(tq, pc, q, n)
+        chunk = data((1, 40, 4, 128), "bf16", 63)  # 160 rows
+        o2 = torch.empty((1, 40, 4, 128), device="cuda")
+        ws = torch.empty(tq.prefill_workspace_size(L.params, 1, 40, n), dtype=torch.uint8, device="cuda")
+        tq.prefill_attention(L.params, pc.cache, 40, chunk, 128**-0.5, o2, None, ws, n)
+        pages, counts = select(tq, pc, q, 5, 1, 1, n)
+        o3 = torch.empty((1, 4, 128), device="cuda")
+        ws = torch.empty(tq.decode_pages_workspace_size(L.params, 1, 5), dtype=torch.uint8, device="cuda")
+        tq.decode_attention_pages(L.params, pc.cache, q, 128**-0.5, pages, counts, 5, o3, None, ws, n)
+        got.append((rk, rv, out, lse, o2, pages, counts, o3))
+    assert tq.check_device_error() == 0
+    assert got[0][0].abs().sum() > 0
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
+def test_a_captured_step_selects_tracks_and_evicts(tq):
+    """One graph of a whole serving step, replayed, against the same calls made one by one."""
+    L = layer(tq, 128, 2, 4, 5)
+    T, steps, budget, n_sel, scale = 150, 40, 6, 3, 128**-0.5
+    k, v = data((2, T + steps, 2, 128), "bf16", 70), data((2, T + steps, 2, 128), "bf16", 71)
+    qs = data((steps, 2, 8, 128), "bf16", 72)
+    mx = T + 16
+
+    def make():
+        pc = tq.PagedCache(L, 2, mx)
+        pc.prefill(k[:, :T], v[:, :T])
+        b = dict(pc=pc, k=k[:, 0].clone(), v=v[:, 0].clone(), q=qs[0].clone(), mass=torch.zeros((2, pc.max_pages), device="cuda"),
+                 pages=torch.zeros((2, 2, n_sel), dtype=torch.int32, device="cuda"),
+                 counts=torch.zeros((2, 2), dtype=torch.int32, device="cuda"),
+                 kept=torch.zeros((2, budget), dtype=torch.int32, device="cuda"), out=torch.zeros((2, 8, 128), device="cuda"),
+                 few=torch.zeros((2, 8, 128), device="cuda"), lse=torch.zeros((2, 8), device="cuda"),
+                 scores=torch.zeros((2, 8, mx), device="cuda"))
+        size = max(tq.select_workspace_size(L.params, 2, mx), tq.decode_pages_workspace_size(L.params, 2, n_sel),
+                   tq.decode_workspace_size(L.params, 2, mx), tq.evict_workspace_size(L.params, 2, pc.max_pages))
+        b["ws"] = torch.empty(size, dtype=torch.uint8, device="cuda")  # one for all: the calls follow one another
+        return b
+
+    def step(b):
+        c = b["pc"].cache
+        b["pc"].append(b["k"], b["v"])
+        tq.select_pages(L.params, c, b["q"], n_sel, 1, 1, b["pages"], b["counts"], b["ws"], mx)
+        tq.decode_attention_pages(L.params, c, b["q"], scale, b["pages"], b["counts"], n_sel, b["few"], None, b["ws"], mx)
+        tq.decode_attention(L.params, c, b["q"], scale, b["out"], b["lse"], b["scores"], b["ws"], mx)
+        tq.track_pages(L.params, c, b["scores"], b["lse"], b["mass"], mx)
+        tq.evict_pages(L.params, c, c, b["mass"], b["mass"], budget, 1, 1, b["kept"], b["ws"])
+
+    eager, played = make(), make()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(played)
+    for t in range(steps):
+        for b in (eager, played):
+            b["k"].copy_(k[:, T + t])
+            b["v"].copy_(v[:, T + t])
+            b["q"].copy_(qs[t])
+        step(eager)
+        graph.replay()
+        for name in ("out", "few", "lse", "mass", "pages", "counts", "kept"):
+            assert torch.equal(eager[name], played[name]), (t, name)
+        for name in ("block_table", "seq_len", "n_compressed"):
+            assert torch.equal(getattr(eager["pc"], name), getattr(played["pc"], name)), (t, name)
+    assert tq.check_device_error() == 0
+    assert played["pc"].n_compressed.tolist() == [budget * 16] * 2
