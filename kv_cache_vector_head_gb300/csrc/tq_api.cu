@@ -425,8 +425,6 @@ extern "C" tq_status tq_prefill_attention(const tq_layer_params* p, const tq_cac
       return cuda_status(launch_int8_decode(K, C, q, dtype, scale, nullptr, nullptr, 0, out, lse, nullptr, workspace, L, max_ctx,
                                             n_query, n_query, st),
                          "tq_prefill_attention");
-    if ((long long)cache->batch * L.n_comp_splits > 65535)
-      return fail(TQ_ERR_INVALID_ARG, "batch times splits must be <= 65535");
     return cuda_status(launch_int8_prefill(K, C, n_query, q, dtype, scale, out, lse, workspace, L, max_ctx, st),
                        "tq_prefill_attention");
   }

@@ -131,4 +131,52 @@ __device__ __forceinline__ float elem_of<__half>(const uint4& w, int i) {
   return __half2float(__ushort_as_half((unsigned short)(i & 1 ? u >> 16 : u & 0xffffu)));
 }
 
+__device__ __forceinline__ float i8_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Joins n partial results of one query head, row(0), row(1) .. in that order; references in powers of two.  D / 4 threads.
+template <int D, typename Row>
+__device__ __forceinline__ void i8_join(const float2* ml, const float4* acc, int n, Row row, float* out, float* lse, int dh) {
+  const int j = threadIdx.x;
+  float M = -INFINITY;
+  for (int s = 0; s < n; ++s) M = fmaxf(M, ml[row(s)].x);
+  const float mb = M == -INFINITY ? 0.f : M;
+  float sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) {
+    const float2 p = ml[row(s)];
+    const float f = i8_ex2(p.x - mb);
+    if (p.y == 0.f) continue;  // a split that saw nothing may not have written its sums
+    const float4 a = acc[row(s) * (D / 4) + j];
+    sum = fmaf(f, p.y, sum);
+    o.x = fmaf(f, a.x, o.x);
+    o.y = fmaf(f, a.y, o.y);
+    o.z = fmaf(f, a.z, o.z);
+    o.w = fmaf(f, a.w, o.w);
+  }
+  const float z = sum == 0.f ? 0.f : 1.f / sum;
+  if (4 * j < dh) *reinterpret_cast<float4*>(out + 4 * j) = make_float4(o.x * z, o.y * z, o.z * z, o.w * z);
+  if (lse && j == 0) *lse = sum == 0.f ? -INFINITY : M * 0.6931471805599453f + logf(sum);
+}
+
+// Launch as a programmatic dependent of the kernel before it in the stream.
+template <typename... K, typename... A>
+cudaError_t i8_launch_after(void (*kern)(K...), dim3 grid, int threads, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<K>(args)...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 }  // namespace tq

@@ -458,56 +458,14 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D))
   }
 }
 
-// Joins n partial results of one query head, row(0), row(1) .. in that order; references in powers of two.  D / 4 threads.
-template <int D, typename Row>
-__device__ __forceinline__ void join(const float2* ml, const float4* acc, int n, Row row, float* out, float* lse, int dh) {
-  const int j = threadIdx.x;
-  float M = -INFINITY;
-  for (int s = 0; s < n; ++s) M = fmaxf(M, ml[row(s)].x);
-  const float mb = M == -INFINITY ? 0.f : M;
-  float sum = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int s = 0; s < n; ++s) {
-    const float2 p = ml[row(s)];
-    const float f = ex2(p.x - mb);
-    if (p.y == 0.f) continue;  // a split that saw nothing may not have written its sums
-    const float4 a = acc[row(s) * (D / 4) + j];
-    sum = fmaf(f, p.y, sum);
-    o.x = fmaf(f, a.x, o.x);
-    o.y = fmaf(f, a.y, o.y);
-    o.z = fmaf(f, a.z, o.z);
-    o.w = fmaf(f, a.w, o.w);
-  }
-  const float z = sum == 0.f ? 0.f : 1.f / sum;
-  if (4 * j < dh) *reinterpret_cast<float4*>(out + 4 * j) = make_float4(o.x * z, o.y * z, o.z * z, o.w * z);
-  if (lse && j == 0) *lse = sum == 0.f ? -INFINITY : M * kLn2 + logf(sum);
-}
-
 // Equal parts of every unit: row = head * splits + split.
 template <int D>
 __global__ void __launch_bounds__(D / 4) i8_combine_kernel(const unsigned char* ws, WsLayout L, int hq, int dh, float* out,
                                                            float* lse) {
   const size_t head = (size_t)blockIdx.y * hq + blockIdx.x, S = L.n_comp_splits;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  join<D>(reinterpret_cast<const float2*>(ws + L.ml), reinterpret_cast<const float4*>(ws + L.acc), L.n_comp_splits,
+  i8_join<D>(reinterpret_cast<const float2*>(ws + L.ml), reinterpret_cast<const float4*>(ws + L.acc), L.n_comp_splits,
           [&](int s) { return head * S + s; }, out + head * dh, lse ? lse + head : nullptr, dh);
-}
-
-// Launch as a programmatic dependent of the kernel before it in the stream.
-template <typename... K, typename... A>
-cudaError_t launch_after(void (*kern)(K...), dim3 grid, int threads, cudaStream_t st, A... args) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(threads);
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, static_cast<K>(args)...);
-  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int D>
@@ -570,7 +528,7 @@ cudaError_t launch_int8_decode(const KParams& P, const KCache& C, const void* q,
 cudaError_t launch_int8_combine(const KParams& P, const unsigned char* ws, const WsLayout& L, long long rows, float* out,
                                 float* lse, cudaStream_t st) {
   auto kern = P.d == 128 ? i8_combine_kernel<128> : i8_combine_kernel<256>;
-  return launch_after(kern, dim3(P.hq, (unsigned)rows), P.d / 4, st, ws, L, P.hq, P.dh, out, lse);
+  return i8_launch_after(kern, dim3(P.hq, (unsigned)rows), P.d / 4, st, ws, L, P.hq, P.dh, out, lse);
 }
 
 cudaError_t read_clear_int8_decode_error(unsigned* bits) {

@@ -27,7 +27,8 @@
 // 4000 (of 16 warps' 13700 instructions an SM issues 1.7 a cycle), then it waits for its own O and next S: the two units
 // cover about half of each other's.  Measured on the way, on the chunk of 2048 queries over 16384 tokens, 32 heads: O in
 // registers after every tile 1283 us (130 registers a thread where 96 are there: the spills go to L2); half tiles of 64
-// tokens, with S of one half during the softmax of the other, 1210 us (every step's waits twice); now 990 us.
+// tokens, with S of one half during the softmax of the other, 1210 us (every step's waits twice); now 990 us, and
+// 916 us with the last wave's units split.
 #include <math.h>
 
 #include <algorithm>
@@ -260,7 +261,8 @@ __device__ __forceinline__ float weights(uint32_t ts, const float2* scales, floa
   return l0 + l1;
 }
 
-// RT row tiles of 128, QL query limbs (RT + QL = 3).  grid (row tiles, hkv, batch * splits).
+// RT row tiles of 128, QL query limbs (RT + QL = 3).  A unit is a block's rows of one (sequence, KV head), row tiles fastest;
+// the first L.whole_units of them are a block each, the others L.n_comp_splits blocks each.
 template <int RT, int QL>
 __global__ void __launch_bounds__(kThreads, 1)
     i8_prefill_attn_kernel(const __grid_constant__ KParams P, const __grid_constant__ KCache C, int n_query, const void* q,
@@ -268,9 +270,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ Shared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = blockIdx.y, S = L.n_comp_splits, b = blockIdx.z / S, split = blockIdx.z % S;
-  const int G = P.G, rows = n_query * G;
-  const int row0 = blockIdx.x * 128 * RT;
+  const int G = P.G, rows = n_query * G, rt = (rows + 128 * RT - 1) / (128 * RT);
+  const int whole = L.whole_units, rest = rt * P.hkv * C.batch - whole, after = (int)blockIdx.x - whole;
+  const int unit = after < 0 ? (int)blockIdx.x : whole + after % rest;
+  const int S = after < 0 ? 1 : L.n_comp_splits, split = after < 0 ? 0 : after / rest;
+  const int row0 = unit % rt * 128 * RT, g = unit / rt % P.hkv, b = unit / rt / P.hkv;
   const uint32_t sbase = smem_u32(smem);
 
   int n = C.seq_len[b], nc = C.n_compressed[b];
@@ -364,8 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool direct = RT == 2 && S == 1;
     const int sx = RT == 2 ? split : 2 * split + u, SX = RT == 2 ? S : 2 * S;
     // where the row's sums gather: four channels of 128 rows side by side, so that a warp's accesses are contiguous
-    const size_t block = ((size_t)blockIdx.z * gridDim.y + g) * gridDim.x + blockIdx.x;
-    float4* gather = reinterpret_cast<float4*>(ws + L.afrag) + ((block * 2 + u) * 2 + hf) * (H / 4 * 128) + r;
+    const size_t place = ((size_t)(unit - whole) * (128 * RT) + (rr - row0)) * SX + sx;  // of the partial results
+    float4* gather = reinterpret_cast<float4*>(ws + L.afrag) + (((size_t)blockIdx.x * 2 + u) * 2 + hf) * (H / 4 * 128) + r;
     // references, in powers of two, of the exponents and, relative to that, of the weights (a page of large values that
     // hardly weighs does not push the others' weights under f16's range); the sum
     float m = -INFINITY, wref = -INFINITY, l = 0.f;
@@ -475,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     l = sh.l[u][0][r] + sh.l[u][1][r];
     // what is gathered and the last O, in true units, to the output row or to the split's partial sums
     const float unit = wref == -INFINITY ? 0.f : ex2(wref) * (1.f / kWeightTop), z = direct ? (l == 0.f ? 0.f : unit / l) : unit;
-    float* dst = direct ? out + head * P.dh + H * hf : reinterpret_cast<float*>(ws + L.acc) + (head * SX + sx) * D + H * hf;
+    float* dst = direct ? out + head * P.dh + H * hf : reinterpret_cast<float*>(ws + L.acc) + place * D + H * hf;
     const int width = rr >= rows ? 0 : direct ? min(H, P.dh - H * hf) : H;  // (a multiple of 4; can be negative)
 #pragma unroll 1
     for (int c = 0; c < H / 16; ++c) {
@@ -499,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (direct) {
         if (lse) lse[head] = l == 0.f ? -INFINITY : m * 0.6931471805599453f + logf(l);
       } else {
-        float* ml = reinterpret_cast<float*>(ws + L.ml) + (head * SX + sx) * 2;
+        float* ml = reinterpret_cast<float*>(ws + L.ml) + place * 2;
         ml[0] = l == 0.f ? -INFINITY : m;  // in powers of two
         ml[1] = l;
       }
@@ -790,50 +794,69 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
 }
 
+// Adds up the splits of the units that have them: block = (unit - whole) * rows of a unit + row, D / 4 threads.
+__global__ void __launch_bounds__(D / 4) i8_prefill_join_kernel(const unsigned char* ws, WsLayout L, int per, int splits, int G,
+                                                                int hkv, int hq, int n_query, int dh, float* out, float* lse) {
+  const int rows = n_query * G, rt = (rows + per - 1) / per;
+  const int unit = L.whole_units + (int)blockIdx.x / per, r = unit % rt * per + (int)blockIdx.x % per;
+  if (r >= rows) return;
+  const int g = unit / rt % hkv, b = unit / rt / hkv;
+  const size_t head = ((size_t)b * n_query + r / G) * hq + (size_t)g * G + r % G, first = (size_t)blockIdx.x * splits;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  i8_join<D>(reinterpret_cast<const float2*>(ws + L.ml), reinterpret_cast<const float4*>(ws + L.acc), splits,
+             [&](int s) { return first + s; }, out + head * dh, lse ? lse + head : nullptr, dh);
+}
+
 }  // namespace
 
 // From 49 rows a KV head on: up to there the decode kernel, eight rows a block, is as fast or faster (8 sequences of 8192
 // tokens, 8 heads: 48 rows 106 us, here 122 us; 64 rows 133 and 126 us; one of 32768 tokens, G = 8: 48 rows 70 and 60 us).
 bool int8_prefill_tc_ok(const KParams& P, int n_query) { return P.d == D && (long long)n_query * P.G > 48; }
 
-// Blocks' rows a KV head, and the places of the gathered sums (afrag) and of the partial results in `splits` splits;
-// returns the bytes they take.
-static size_t places(const KParams& P, int batch, int n_query, int splits, bool one, WsLayout* L) {
+// Places of the gathered sums (afrag) and of the partial results where the first `whole` units are a block each and the
+// others `splits`; returns the bytes they take.
+static size_t places(const KParams& P, int batch, int n_query, int whole, int splits, bool one, WsLayout* L) {
   const int S = one ? 2 * splits : splits, per = one ? 128 : 256;
-  const size_t heads = (size_t)batch * n_query * P.hq;
-  const size_t blocks = ((size_t)n_query * P.G + per - 1) / per * P.hkv * batch * splits;
+  const size_t rest = ((size_t)n_query * P.G + per - 1) / per * P.hkv * batch - whole;
   L->n_comp_splits = splits;
+  L->whole_units = whole;
   L->afrag = 0;
-  size_t o = blocks * 256 * D * sizeof(float);
+  size_t o = (whole + rest * splits) * 256 * D * sizeof(float);
   L->ml = o;
-  if (S > 1) o += (heads * S * 2 * sizeof(float) + 255) & ~(size_t)255;
+  if (S > 1) o += (rest * per * S * 2 * sizeof(float) + 255) & ~(size_t)255;
   L->acc = o;
-  if (S > 1) o += (heads * S * (size_t)D * sizeof(float) + 255) & ~(size_t)255;
+  if (S > 1) o += rest * per * S * (size_t)D * sizeof(float);
   return o;
 }
 
-// Splits of the key tiles: blocks are one to an SM, so the count whose last wave is fullest, at least four tiles
-// a split.  A split costs about 6.5 % of a block's work (its start, and a pass over its partial outputs): the chunk of 2048
-// queries over 16384 tokens, 256 blocks of two row tiles, takes 930 us whole (1.7 waves), 959 us in four splits (6.7; both with O begun anew every eight tiles).
+// Splits of the key tiles: blocks are one to an SM, so the counts that leave the least time after full waves, at least
+// four tiles a split; either of all units, or (two row tiles) of those behind the last full wave of whole ones.  A split
+// costs 4.5 to 6.5 % of a block's work (its start, and a pass over its partial outputs).  The chunk of 2048 queries over
+// 16384 tokens, 256 blocks of two row tiles: all whole (1.7 waves) 990 us; the last 104 in four splits 916 us.  (So a
+// query's sums may be cut elsewhere at another place of the batch: equal to rounding, not to the bit.)
 WsLayout int8_prefill_layout(const KParams& P, int batch, int n_query, int max_ctx, int num_sms) {
   const long long rt = ((long long)n_query * P.G + 255) / 256, units = std::max(1LL, rt * batch * P.hkv);
   const int tiles = std::max(1, (max_ctx + KT - 1) / KT);
-  int best = 1;
-  double best_eff = -1.0;
+  const long long sms = std::max(1, num_sms), waves = units / sms;
+  WsLayout L{};
+  double best = 1e30, mixed = 1e30;
   for (int S = 1; S <= 64; ++S) {
-    if (S > 1 && tiles / S < 4) break;
-    if (units * S > 65535) break;
-    const double w = (double)(units * S) / std::max(1, num_sms);
-    const double eff = w / ceil(w) / (1.0 + 0.065 * (S - 1));
-    if (eff > best_eff + 1e-9) {
-      best_eff = eff;
-      best = S;
+    if (S > 1 && (tiles / S < 4 || units * S > 65535)) break;
+    auto time = [&](long long n) { return (double)((n * S + sms - 1) / sms) / S * (1.0 + 0.065 * (S - 1)); };
+    if (time(units) < best - 1e-9) {
+      best = time(units);
+      L.n_comp_splits = S;
+    }
+    if (waves > 0 && S > 1 && units > waves * sms && waves + time(units - waves * sms) < mixed - 1e-9) {
+      mixed = waves + time(units - waves * sms);
+      L.rest_splits = S;
     }
   }
-  WsLayout L{};
+  L.whole_units = mixed < best ? (int)(waves * sms) : 0;
   // room for either kind of block: the queries' type is not known here
-  const size_t one = places(P, batch, n_query, best, true, &L);
-  L.total = std::max(one, places(P, batch, n_query, best, false, &L));
+  WsLayout K{};
+  const size_t one = places(P, batch, n_query, 0, L.n_comp_splits, true, &K);
+  L.total = std::max(one, places(P, batch, n_query, L.whole_units, L.whole_units ? L.rest_splits : L.n_comp_splits, false, &K));
   return L;
 }
 
@@ -847,14 +870,16 @@ cudaError_t launch_int8_prefill(const KParams& P, const KCache& C, int n_query, 
   cudaError_t e = allow_dynamic_smem((const void*)kern, kSmemBytes);
   if (e != cudaSuccess) return e;
   const int per = one ? 128 : 256;
-  WsLayout K{}, J;
-  places(P, C.batch, n_query, L.n_comp_splits, one, &K);
-  J = K;  // the joining kernel's splits
-  J.n_comp_splits = one ? 2 * L.n_comp_splits : L.n_comp_splits;
-  kern<<<dim3((rows + per - 1) / per, P.hkv, C.batch * L.n_comp_splits), kThreads, kSmemBytes, st>>>(P, C, n_query, q, dtype, scale,
-                                                                                                 out, lse, w, K, max_ctx);
-  if ((e = cudaGetLastError()) != cudaSuccess || J.n_comp_splits == 1) return e;
-  return launch_int8_combine(P, w, J, (long long)C.batch * n_query, out, lse, st);
+  const int whole = one ? 0 : L.whole_units, splits = whole ? L.rest_splits : L.n_comp_splits;
+  WsLayout K{};
+  places(P, C.batch, n_query, whole, splits, one, &K);
+  const unsigned rest = (unsigned)((rows + per - 1) / per * P.hkv * C.batch - whole);
+  kern<<<whole + rest * splits, kThreads, kSmemBytes, st>>>(P, C, n_query, q, dtype, scale, out, lse, w, K, max_ctx);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int parts = one ? 2 * splits : splits;
+  if (parts == 1) return cudaSuccess;
+  return i8_launch_after(i8_prefill_join_kernel, dim3(rest * per), D / 4, st, w, K, per, parts, P.G, P.hkv, P.hq, n_query, P.dh,
+                         out, lse);
 }
 
 cudaError_t read_clear_int8_prefill_error(unsigned* bits) {

@@ -28,6 +28,7 @@ struct WsLayout {
   size_t afrag_bytes_per_head;  // per (sequence, kv head)
   int n_comp_splits;   // compressed-page splits; one extra split holds the window
   int pages_per_split;
+  int whole_units, rest_splits;  // (8-bit chunks) the first units whole, the others in so many splits; 0: not so
 };
 WsLayout decode_ws_layout(const KParams& P, int batch, int max_ctx, int n_splits, int num_sms);
 

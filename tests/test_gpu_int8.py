@@ -497,6 +497,43 @@ def test_prefill_attention_of_ragged_sequences(tq, nq):
                 check_attention(f64(q)[b, i, h], f64(out)[b, i, h], float(lse[b, i, h]), kk[:see], vv[:see], 128**-0.5, (b, h, i))
 
 
+@pytest.mark.parametrize("B,hkv,g,nq,T,window,dtype,seqs,heads,queries", [
+    (39, 4, 2, 65, 1100, 16, "bf16", (0, 36, 37, 38), (0, 5, 7), (0, 63, 64)),
+    (1, 8, 8, 640, 1070, 5, "f16", (0,), (0, 55, 56, 63), (0, 1, 383, 384, 385, 639)),
+    (39, 4, 2, 65, 1100, 16, "f32", (0, 38), (0, 7), (0, 64)),
+])
+def test_prefill_attention_of_more_row_tiles_than_places(tq, B, hkv, g, nq, T, window, dtype, seqs, heads, queries):
+    """156 and 160 units of work: those behind the last full wave are split over the keys."""
+    L = layer(tq, 128, hkv, g, window)
+    lens = [T - 3 * (b % 11) for b in range(B)]
+    k = data((B, T, hkv, 128), dtype, 27)
+    pc = tq.PagedCache(L, B, T)
+    for b, n in enumerate(lens):
+        one = tq.PagedCache(L, 1, T, pool_pages=1)
+        one.share_pages(pc)
+        one.block_table.copy_(pc.block_table[b:b + 1])
+        one.prefill(k[b:b + 1, :n].contiguous(), k[b:b + 1, :n].contiguous())
+        pc.seq_len[b], pc.n_compressed[b] = n, O8.n_compressed(n, window)
+        pc.win_k[b], pc.win_v[b] = one.win_k[0], one.win_v[0]
+    q = data((B, nq, hkv * g, 128), dtype, 28)
+    ws = torch.empty(tq.prefill_workspace_size(L.params, B, nq, T), dtype=torch.uint8, device="cuda")
+    out, lse = torch.full(q.shape, float("nan"), device="cuda"), torch.full(q.shape[:-1], float("nan"), device="cuda")
+    tq.prefill_attention(L.params, pc.cache, nq, q, 128**-0.5, out, lse, ws, T)
+    assert tq.check_device_error() == 0
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    again = torch.empty_like(out)
+    tq.prefill_attention(L.params, pc.cache, nq, q, 128**-0.5, again, None, ws, T)
+    assert torch.equal(out, again)
+    for b in seqs:
+        n = lens[b]
+        m = Mirror(L, k[b:b + 1], k[b:b + 1])
+        for h in heads:
+            kk, vv = m.values(0, h // g, n, n)
+            for i in queries:
+                see = n - nq + i + 1
+                check_attention(f64(q[b, i, h]), f64(out[b, i, h]), float(lse[b, i, h]), kk[:see], vv[:see], 128**-0.5, (b, h, i))
+
+
 def test_chunked_prefill_equals_decode_of_its_last_query(tq):
     """The chunk's last query is a decode query: both calls within the tolerance of the same definition."""
     L = layer(tq, 128, 4, 4, 32)
