@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const __grid_co
 constexpr int kTrackWarps = 8;
 
 // Pages that `tokens` >= 0 tokens take.  Counters may hold anything: the rounding up must not pass 32 bits.
-__device__ __forceinline__ int pages_of(int tokens) { return tokens / kPage + (tokens % kPage ? 1 : 0); }
+__device__ __forceinline__ int pages_of(int tokens) { return (int)(((unsigned)tokens + kPage - 1u) / kPage); }
 
 // One block eight pages (128 tokens, four lanes of four tokens a page), its warps take the heads in turn.
 template <bool VEC>
@@ -397,8 +397,9 @@ __global__ void __launch_bounds__(256) evict_window_kernel(const __grid_constant
 
 // Blocks x = 0, one a sequence: block table (kept pages in order, a partly filled page, the dropped pages, the rest),
 // masses, counters.  New rows are put together in the workspace first, as the outputs may be the inputs.  Where they
-// are not, blocks x > 0 move the windows in the same launch.
-__global__ void __launch_bounds__(kPickThreads) evict_pick_kernel(const __grid_constant__ KCache A,
+// are not, blocks x > 0 move the windows in the same launch: short blocks, so two an SM (32 registers; at one, 64
+// registers, 32 x 16384 tokens to 512 pages take 20.5 us in place of 16.5).
+__global__ void __launch_bounds__(kPickThreads, 2) evict_pick_kernel(const __grid_constant__ KCache A,
                                                                   const __grid_constant__ KCache B, const float* mass,
                                                                   float* mass_out, int budget, int n_sink, int n_recent,
                                                                   int32_t* kept, int32_t* ws, int hkv, int d) {
